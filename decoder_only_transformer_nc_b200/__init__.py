@@ -21,7 +21,8 @@ __all__ = [
     "loss_mean", "cast_weights", "selftest_bounded_wait", "BF16", "F16", "F32",
     "fp8_quantize", "linear_fp8", "FP8_BLOCK", "FP8_LM_HEAD", "FP8_ALL",
     "train_workspace_bytes", "forward_backward", "linear_dgrad", "linear_wgrad", "attention_lse",
-    "attention_backward",
+    "attention_backward", "tree_mask", "tree_attention", "sample", "tree_accept", "distill_topk",
+    "tree_workspace_bytes", "Session",
     "EPI_STORE_16", "EPI_RELU2_16", "EPI_RESID_F32", "EPI_STORE_F32", "EPI_SOFTCAP_F32",
 ]
 
@@ -154,6 +155,15 @@ def lib():
             "nc_prefill": (i32, [cfgp, ctypes.POINTER(NcWeights), vp, i32, i32, vp, vp, sz, i32, vp, sz, vp]),
             "nc_decode_step": (i32, [cfgp, ctypes.POINTER(NcWeights), vp, i32, i32, vp, vp, sz, i32, vp]),
             "nc_decode_step_dev": (i32, [cfgp, ctypes.POINTER(NcWeights), vp, i32, vp, vp, vp, sz, i32, vp]),
+            "nc_tree_workspace_bytes": (sz, [cfgp, i32, i32]),
+            "nc_decode_tree": (i32, [cfgp, ctypes.POINTER(NcWeights), vp, vp, vp, i32, i32, vp, vp, sz, i32, vp, sz,
+                                     vp]),
+            "nc_accept_tree": (i32, [cfgp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, i32, vp, sz, vp]),
+            "nc_tree_mask": (i32, [vp, vp, i32, i32, vp]),
+            "nc_tree_attention": (i32, [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]),
+            "nc_tree_accept": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
+            "nc_sample": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp]),
+            "nc_distill_topk": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -338,6 +348,7 @@ class Session:
         self.buffer = torch.empty(n, dtype=torch.uint8, device=device)
         self.pos = 0
         self._graph = None
+        self._lens = self._tree = self._tree_ws = None
 
     def prefill(self, tokens, want_logits=False, stream=None):
         """Runs the prompt tokens [B, T]; returns the logits [B, T, V] if asked."""
@@ -351,12 +362,14 @@ class Session:
                                 _ptr(logits), _ptr(self.buffer), self.buffer.numel(), self.T_max, _ptr(ws),
                                 ws.numel(), _stream(stream)), "nc_prefill")
         self.pos = T
+        self._lens = self._tree = None
         return logits
 
     def decode(self, tokens, logits=None, stream=None):
         """One position for every row: tokens [B] int32; returns logits [B, V]."""
         import torch
         cfg = self.model.cfg
+        self._one_length("Session.decode")
         if logits is None:
             logits = torch.empty((self.B, cfg.vocab), dtype=torch.float32, device=tokens.device)
         _check(lib().nc_decode_step(ctypes.byref(cfg), ctypes.byref(self.model.weights), _ptr(tokens), self.B,
@@ -364,6 +377,75 @@ class Session:
                                     _stream(stream)), "nc_decode_step")
         self.pos += 1
         return logits
+
+    def _one_length(self, where):
+        """decode and decode_graph move every row by one position from a common length."""
+        if self.pos is None:
+            raise NcError(1, f"{where}: the rows have lengths of their own after accept_tree (decode_tree goes on)")
+        self._tree = None
+
+    @property
+    def lens(self):
+        """Committed positions of every row: int32 CUDA tensor [B]."""
+        import torch
+        if self._lens is not None:
+            return self._lens
+        return torch.full((self.B,), self.pos, dtype=torch.int32, device=self.buffer.device)
+
+    def decode_tree(self, tokens, parents, logits=None, stream=None):
+        """Logits [B, N, V] of a tree of drafted tokens a row (nc_decode_tree).
+
+        tokens, parents: int32 [B, N], N <= 128; parents[b, i] < i is node i's
+        parent, -1 for a root, -2 for an unused node.  Node 0 is the row's next
+        token.  ``accept_tree`` then moves the path that the samples confirm
+        into the cache; without it the tree is dropped."""
+        import torch
+        cfg, dev = self.model.cfg, self.buffer.device
+        where = "Session.decode_tree"
+        if tokens.dim() != 2 or tokens.shape[0] != self.B:
+            raise NcError(3, f"{where}: tokens {tuple(tokens.shape)}, rows {self.B}")
+        N = tokens.shape[1]
+        need = tree_workspace_bytes(cfg, self.B, N)
+        if need == 0:
+            raise NcError(3, f"{where}: {N} nodes a row")
+        tp = _arg(where, "tokens", tokens, torch.int32, (self.B, N), dev)
+        pp = _arg(where, "parents", parents, torch.int32, (self.B, N), dev)
+        with _allocate_on(stream):
+            lens = self.lens
+            if self._tree_ws is None or self._tree_ws.numel() < need:
+                self._tree_ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            if logits is None:
+                logits = torch.empty((self.B, N, cfg.vocab), dtype=torch.float32, device=dev)
+        lp = _arg(where, "logits", logits, torch.float32, (self.B, N, cfg.vocab), dev)
+        self._tree = None
+        _launch(where, dev, stream, lib().nc_decode_tree, ctypes.byref(cfg), ctypes.byref(self.model.weights), tp, pp,
+                lens.data_ptr(), self.B, N, lp, self.buffer.data_ptr(), self.buffer.numel(), self.T_max,
+                self._tree_ws.data_ptr(), self._tree_ws.numel())
+        self._tree = (tokens, parents, lens)
+        return logits
+
+    def accept_tree(self, sampled, stream=None):
+        """Accepts the path of the last decode_tree that ``sampled`` (int32 [B, N],
+        the token sampled at each node) confirms and moves its keys and values
+        into the cache (nc_accept_tree).  Returns (path [B, N], count [B], next
+        [B]): the accepted nodes (then -1), how many, and the token sampled at the
+        last of them -- node 0 of the row's next tree."""
+        import torch
+        where = "Session.accept_tree"
+        if self._tree is None:
+            raise NcError(1, f"{where}: no decode_tree before it")
+        tokens, parents, lens = self._tree
+        dev, N = self.buffer.device, tokens.shape[1]
+        sp = _arg(where, "sampled", sampled, torch.int32, (self.B, N), dev)
+        with _allocate_on(stream):
+            path = torch.empty((self.B, N), dtype=torch.int32, device=dev)
+            count, nxt, lens_out = (torch.empty(self.B, dtype=torch.int32, device=dev) for _ in range(3))
+        _launch(where, dev, stream, lib().nc_accept_tree, ctypes.byref(self.model.cfg), tokens.data_ptr(),
+                parents.data_ptr(), sp, lens.data_ptr(), self.B, N, path.data_ptr(), count.data_ptr(), nxt.data_ptr(),
+                lens_out.data_ptr(), self.buffer.data_ptr(), self.buffer.numel(), self.T_max,
+                self._tree_ws.data_ptr(), self._tree_ws.numel())
+        self._tree, self._lens, self.pos = None, lens_out, None
+        return path, count, nxt
 
     def _step_dev(self, stream=None):
         cfg = self.model.cfg
@@ -379,6 +461,7 @@ class Session:
         next step.  The first call runs the step eagerly, then captures it.
         Raises NcError(NC_ERR_SHAPE) once every cache position is used."""
         import torch
+        self._one_length("Session.decode_graph")
         if self.pos >= self.T_max:
             raise NcError(3, f"Session.decode_graph: position {self.pos} is past the cache (T_max {self.T_max})")
         if self._graph is None:
@@ -646,3 +729,171 @@ def selftest_bounded_wait(status, limit_us=20000, stream=None):
 def loss_mean(token_loss, targets, V, loss, stream=None):
     _check(lib().nc_loss_mean(_ptr(token_loss), _ptr(targets), token_loss.numel(), V, _ptr(loss),
                               _stream(stream)), "nc_loss_mean")
+
+
+# ---------------------------------------------------------------- drafted trees, sampling, distillation
+
+def _arg(where, name, t, dtype, shape, dev):
+    """Checks one tensor argument; returns its address (0 for an absent one)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise NcError(3, f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise NcError(1, f"{where}: {name} is not contiguous")
+    if t.device != dev:
+        raise NcError(1, f"{where}: {name} is on {t.device}, expected {dev}")
+    return t.data_ptr()
+
+
+def _launch(where, dev, stream, fn, *args):
+    """Calls a library function on the tensors' device, on ``stream`` (of that
+    device) or its current stream."""
+    import torch
+    if dev.type != "cuda":
+        raise NcError(8, f"{where}: tensors are on {dev}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise NcError(1, f"{where}: the stream is on {stream.device}, the tensors are on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream.cuda_stream)
+    if code != 0:
+        raise NcError(code, where)
+
+
+def _allocate_on(stream):
+    """Context in which new tensors belong to ``stream`` (None: the current one)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def tree_workspace_bytes(c: NcConfig, B: int, N: int) -> int:
+    return lib().nc_tree_workspace_bytes(ctypes.byref(c), B, N)
+
+
+def tree_mask(parents, mask, stream=None):
+    """Ancestor words [B, N, ceil(N / 32)] int32 of the trees ``parents`` [B, N] int32 (nc_tree_mask)."""
+    import torch
+    where = "tree_mask"
+    if parents.dim() != 2:
+        raise NcError(3, f"{where}: parents {tuple(parents.shape)}")
+    B, N = parents.shape
+    dev = parents.device
+    a = (_arg(where, "parents", parents, torch.int32, (B, N), dev),
+         _arg(where, "mask", mask, torch.int32, (B, N, (N + 31) // 32), dev))
+    _launch(where, dev, stream, lib().nc_tree_mask, *a, B, N)
+
+
+def tree_attention(q, kv, cache, lens, mask, out, window=0, stream=None):
+    """Attention of the drafted nodes of every row over the cache and their
+    ancestors (nc_tree_attention).
+
+    q [B, N, H, D] (the nodes may be strided), kv [B, N, 2, Hkv, D], cache
+    [B, T_max, 2, Hkv, D], out [B, N, H, D]: fp16 or bf16; lens [B] int32, mask
+    [B, N, ceil(N / 32)] int32 (tree_mask)."""
+    import torch
+    where = "tree_attention"
+    if q.dim() != 4 or cache.dim() != 5:
+        raise NcError(3, f"{where}: q {tuple(q.shape)}, cache {tuple(cache.shape)}")
+    B, N, H, D = q.shape
+    T_max, Hkv = cache.shape[1], cache.shape[3]
+    dev, dt = q.device, q.dtype
+    qs = H * D
+    if not q.is_contiguous():  # e.g. the q columns of a packed q | k | v
+        qs = q.stride(1) if N > 1 else (q.stride(0) if B > 1 else qs)
+        if q.stride(3) != 1 or (H > 1 and q.stride(2) != D) or (B > 1 and q.stride(0) != N * qs):
+            raise NcError(1, f"{where}: q strides {q.stride()}: only the nodes may be strided")
+    a = (_arg(where, "kv", kv, dt, (B, N, 2, Hkv, D), dev), _arg(where, "cache", cache, dt, (B, T_max, 2, Hkv, D), dev),
+         _arg(where, "lens", lens, torch.int32, (B,), dev),
+         _arg(where, "mask", mask, torch.int32, (B, N, (N + 31) // 32), dev),
+         _arg(where, "out", out, dt, (B, N, H, D), dev))
+    if B:
+        _launch(where, dev, stream, lib().nc_tree_attention, q.data_ptr(), qs, *a, B, N, H, Hkv, D, T_max, window,
+                _dt(q))
+
+
+def sample(logits, u, tokens, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """One token a row from logits [M, V] fp32 (rows may be strided) and uniform
+    numbers u [M] fp32 into tokens [M] int32 and logprob [M] fp32 (nc_sample).
+    temperature, top_p, min_p: [M] fp32 or None; top_k: [M] int32 or None."""
+    import torch
+    where = "sample"
+    if logits.dim() != 2:
+        raise NcError(3, f"{where}: logits {tuple(logits.shape)}")
+    if logits.dtype is not torch.float32:
+        raise TypeError(f"{where}: logits are {logits.dtype}, expected torch.float32")
+    M, V = logits.shape
+    ld = logits.stride(0) if M > 1 else V
+    if V > 1 and logits.stride(1) != 1 or ld < V:
+        raise NcError(1, f"{where}: logits strides {logits.stride()}: only the rows may be strided")
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    if u is None or tokens is None:
+        raise NcError(1, f"{where}: u and tokens are needed")
+    a = (_arg(where, "u", u, f32, (M,), dev), _arg(where, "temperature", temperature, f32, (M,), dev),
+         _arg(where, "top_k", top_k, i32, (M,), dev), _arg(where, "top_p", top_p, f32, (M,), dev),
+         _arg(where, "min_p", min_p, f32, (M,), dev), _arg(where, "tokens", tokens, i32, (M,), dev),
+         _arg(where, "logprob", logprob, f32, (M,), dev))
+    if M:
+        _launch(where, dev, stream, lib().nc_sample, logits.data_ptr(), ld, *a, M, V)
+
+
+def tree_accept(tokens, parents, mask, sampled, lens, kv, cache, path, count, next, lens_out, stream=None):
+    """The accepted path of each row's tree, and its K/V moved into the cache
+    (nc_tree_accept).
+
+    tokens, parents, sampled, path [B, N] int32, mask [B, N, ceil(N / 32)]
+    int32, lens, count, next, lens_out [B] int32; kv [L, B, N, 2, Hkv, D] and
+    cache [L, B, T_max, 2, Hkv, D] fp16 or bf16."""
+    import torch
+    where = "tree_accept"
+    if kv.dim() != 6 or cache.dim() != 6:
+        raise NcError(3, f"{where}: kv {tuple(kv.shape)}, cache {tuple(cache.shape)}")
+    L, B, N, _, Hkv, D = kv.shape
+    T_max = cache.shape[2]
+    _dt(kv)
+    dev, i32, bn, b1 = kv.device, torch.int32, (B, N), (B,)
+    a = (_arg(where, "tokens", tokens, i32, bn, dev), _arg(where, "parents", parents, i32, bn, dev),
+         _arg(where, "mask", mask, i32, (B, N, (N + 31) // 32), dev), _arg(where, "sampled", sampled, i32, bn, dev),
+         _arg(where, "lens", lens, i32, b1, dev), _arg(where, "kv", kv, kv.dtype, (L, B, N, 2, Hkv, D), dev),
+         _arg(where, "cache", cache, kv.dtype, (L, B, T_max, 2, Hkv, D), dev),
+         _arg(where, "path", path, i32, bn, dev), _arg(where, "count", count, i32, b1, dev),
+         _arg(where, "next", next, i32, b1, dev), _arg(where, "lens_out", lens_out, i32, b1, dev))
+    if B:
+        _launch(where, dev, stream, lib().nc_tree_accept, *a, B, N, L, Hkv, D, T_max)
+
+
+def distill_topk(z, teacher_idx, teacher_logits, token_loss, dz=None, tau=1.0, cap=15.0, row_weight=None, status=None,
+                 stream=None):
+    """Distillation from a teacher's K largest logits a row: the loss, and with
+    dz its gradient with respect to the raw logits z (nc_distill_topk).
+
+    z [M, V] fp32; teacher_idx [M, K] int32 (-1: unused), teacher_logits [M, K],
+    token_loss [M] and row_weight [M] fp32; dz [M, V] fp32, bf16 or fp16; status:
+    a device status word (int32 or uint8 tensor) or None."""
+    import torch
+    where = "distill_topk"
+    if z.dim() != 2 or teacher_idx.dim() != 2:
+        raise NcError(3, f"{where}: z {tuple(z.shape)}, teacher_idx {tuple(teacher_idx.shape)}")
+    M, V = z.shape
+    K = teacher_idx.shape[1]
+    dev, f32 = z.device, torch.float32
+    if token_loss is None or teacher_logits is None:
+        raise NcError(1, f"{where}: teacher_logits and token_loss are needed")
+    a = (_arg(where, "z", z, f32, (M, V), dev), _arg(where, "teacher_idx", teacher_idx, torch.int32, (M, K), dev),
+         _arg(where, "teacher_logits", teacher_logits, f32, (M, K), dev),
+         _arg(where, "row_weight", row_weight, f32, (M,), dev), _arg(where, "token_loss", token_loss, f32, (M,), dev))
+    if dz is None:
+        dzp, kind = 0, 3
+    else:
+        kind = F32 if dz.dtype is f32 else _dt(dz)
+        dzp = _arg(where, "dz", dz, dz.dtype, (M, V), dev)
+    if M:
+        _launch(where, dev, stream, lib().nc_distill_topk, *a, dzp, kind, M, V, K, tau, cap,
+                None if status is None else status.data_ptr())

@@ -1092,6 +1092,254 @@ nc_status nc_decode_step_dev(const nc_config* cfg, const nc_weights* w, const in
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- drafted trees, sampling, distillation
+extern "C" {
+
+nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, void* stream) {
+  if (!parents || !mask || B < 0) return NC_ERR_INVALID_ARG;
+  if (N < 1 || N > kTreeMaxNodes) return NC_ERR_SHAPE;
+  if (nc_status s = device_ok()) return s;
+  return tree_mask_launch(parents, mask, B, N, S(stream));
+}
+
+nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
+                            const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
+                            int D, int T_max, int window, nc_dtype dtype, void* stream) {
+  if (!q || !kv || !cache || !lens || !mask || !out || B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || !dtype_ok(dtype))
+    return NC_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || N < 1 || N > kTreeMaxNodes || T_max < 1 || B > 65535 || H > 4096) return NC_ERR_SHAPE;
+  if (q_row_stride < (int64_t)H * D || q_row_stride % 8) return NC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(cache) || !aligned16(out)) return NC_ERR_ALIGNMENT;
+  if (nc_status s = device_ok()) return s;
+  return tree_attention_launch(q, q_row_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window,
+                               dtype == NC_F16, S(stream));
+}
+
+nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const uint32_t* mask, const int32_t* sampled,
+                         const int32_t* lens, const uint16_t* kv, uint16_t* cache, int32_t* path, int32_t* count,
+                         int32_t* next, int32_t* lens_out, int B, int N, int L, int Hkv, int D, int T_max,
+                         void* stream) {
+  if (!tokens || !parents || !mask || !sampled || !lens || !kv || !cache || !path || !count || !next || !lens_out ||
+      lens_out == lens || B < 0 || Hkv < 1 || D < 1)
+    return NC_ERR_INVALID_ARG;
+  if (N < 1 || N > kTreeMaxNodes || L < 1 || L > 65535 || T_max < 1 || (int64_t)Hkv * D > (1 << 24) ||
+      (int64_t)Hkv * D % 4 != 0)
+    return NC_ERR_SHAPE;
+  if (!aligned16(kv) || !aligned16(cache)) return NC_ERR_ALIGNMENT;
+  if (nc_status s = device_ok()) return s;
+  return tree_accept_launch(tokens, parents, mask, sampled, lens, kv, cache, path, count, next, lens_out, nullptr, B,
+                            N, L, T_max, 2 * Hkv * D, S(stream));
+}
+
+nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, float* logprob,
+                    int M, int V, void* stream) {
+  if (!logits || !u || !tokens || M < 0) return NC_ERR_INVALID_ARG;
+  if (V < 1 || V > (1 << 24)) return NC_ERR_SHAPE;
+  if (row_stride < V) return NC_ERR_INVALID_ARG;
+  if (nc_status s = device_ok()) return s;
+  return sample_launch(logits, row_stride, u, temperature, top_k, top_p, min_p, tokens, logprob, M, V, S(stream));
+}
+
+nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const float* teacher_logits,
+                          const float* row_weight, float* token_loss, void* dz, nc_grad_dtype dz_dtype, int M, int V,
+                          int K, float tau, float cap, uint32_t* dev_status, void* stream) {
+  if (!z || !teacher_idx || !teacher_logits || !token_loss || M < 0 || !(tau > 0.0f) || !std::isfinite(tau) ||
+      !(cap >= 0.0f) || !std::isfinite(cap) || (int)dz_dtype < NC_GRAD_BF16 || (int)dz_dtype > NC_GRAD_NONE ||
+      (dz == nullptr) != (dz_dtype == NC_GRAD_NONE) || dz == z)
+    return NC_ERR_INVALID_ARG;
+  if (V < 1 || K < 1 || K > 1024) return NC_ERR_SHAPE;
+  if (nc_status s = device_ok()) return s;
+  const int kind = dz_dtype == NC_GRAD_NONE ? 0 : dz_dtype == NC_GRAD_F32 ? 1 : dz_dtype == NC_GRAD_BF16 ? 2 : 3;
+  return distill_topk_launch(z, teacher_idx, teacher_logits, row_weight, token_loss, dz, kind, M, V, K, tau, cap,
+                             dev_status, S(stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of a drafted-tree step over a session: the ancestor words, every
+// layer's drafted K/V [B][N][2][Hkv][D] (kept for the acceptance) and the
+// step's activations for B N rows.  Offsets are 256-byte aligned.
+struct TreeLayout {
+  size_t mask, kv, x, a, q, o, h, acc, x0, xmid, total;
+  size_t kv_layer_elems;
+};
+
+TreeLayout tree_layout(const nc_config* c, int B, int N) {
+  TreeLayout L;
+  const size_t C = c->d_model, D = c->head_dim, H = c->n_head, Hkv = c->n_kv_head, M = (size_t)B * N;
+  const size_t nqkv = (H + 2 * Hkv) * D;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  L.kv_layer_elems = M * 2 * Hkv * D;
+  L.mask = take(M * (size_t)((N + 31) / 32) * 4);
+  L.kv = take(c->n_layer * L.kv_layer_elems * 2);
+  L.x = take(M * C * 4);
+  L.a = take(M * C * 2);
+  L.q = take(M * H * D * 2);
+  L.o = take(M * H * D * 2);
+  L.h = take(M * 4 * C * 2);
+  L.acc = take(M * (nqkv > 4 * C ? nqkv : 4 * C) * 4);
+  L.x0 = (c->extras & NC_EXTRA_RESID_LAMBDAS) ? take(M * C * 4) : 0;
+  L.xmid = (c->extras & NC_EXTRA_BACKOUT) ? take(M * C * 4) : 0;
+  L.total = off;
+  return L;
+}
+
+bool tree_shape_ok(int B, int N) {
+  return B >= 1 && B <= 65535 && N >= 1 && N <= kTreeMaxNodes && (int64_t)B * N <= (1 << 20);
+}
+
+nc_status tree_step_check(const nc_config* cfg, int B, int N, const void* session, size_t session_bytes, int T_max,
+                          const void* workspace, size_t ws_bytes) {
+  if (!config_ok(cfg) || cfg->fp8 != 0) return NC_ERR_CONFIG;
+  if (!tree_shape_ok(B, N) || T_max < 1 || T_max > cfg->seq_len || cfg->n_head > 4096) return NC_ERR_SHAPE;
+  if (session_bytes < session_layout(cfg, B, T_max).total || ws_bytes < tree_layout(cfg, B, N).total)
+    return NC_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(session) & 255u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NC_ERR_ALIGNMENT;
+  return NC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nc_tree_workspace_bytes(const nc_config* cfg, int B, int N) {
+  if (!config_ok(cfg) || !tree_shape_ok(B, N)) return 0;
+  return tree_layout(cfg, B, N).total;
+}
+
+nc_status nc_decode_tree(const nc_config* cfg, const nc_weights* w, const int32_t* tokens, const int32_t* parents,
+                         const int32_t* lens, int B, int N, float* logits, void* session, size_t session_bytes,
+                         int T_max, void* workspace, size_t ws_bytes, void* stream) {
+  if (!cfg || !w || !w->wte || !tokens || !parents || !lens || !logits || !session || !workspace)
+    return NC_ERR_INVALID_ARG;
+  if (nc_status s = tree_step_check(cfg, B, N, session, session_bytes, T_max, workspace, ws_bytes)) return s;
+  if (!aligned16(w->wte) || !aligned16(logits)) return NC_ERR_ALIGNMENT;
+  if (nc_status s = check_extras(cfg, w)) return s;
+  if (nc_status s = device_ok()) return s;
+
+  const SessionLayout SL = session_layout(cfg, B, T_max);
+  const TreeLayout TL = tree_layout(cfg, B, N);
+  cudaStream_t st = S(stream);
+  uint8_t* base = static_cast<uint8_t*>(session);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* status = reinterpret_cast<uint32_t*>(base + SL.status);
+  const float* rope = reinterpret_cast<const float*>(base + SL.rope);
+  const uint16_t* wqkv = reinterpret_cast<const uint16_t*>(base + SL.wqkv);
+  const uint16_t* wo = reinterpret_cast<const uint16_t*>(base + SL.wo);
+  const uint16_t* wfc = reinterpret_cast<const uint16_t*>(base + SL.wfc);
+  const uint16_t* wmp = reinterpret_cast<const uint16_t*>(base + SL.wmp);
+  const uint16_t* wlm = reinterpret_cast<const uint16_t*>(base + SL.wlm);
+  const uint16_t* cache = reinterpret_cast<const uint16_t*>(base + SL.cache);
+  const uint32_t ex = cfg->extras;
+  const int32_t* hist = (ex & NC_EXTRA_SMEAR) ? reinterpret_cast<const int32_t*>(base + SL.hist) : nullptr;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(ws + TL.mask);
+  uint16_t* kv = reinterpret_cast<uint16_t*>(ws + TL.kv);
+  float* x = reinterpret_cast<float*>(ws + TL.x);
+  uint16_t* a = reinterpret_cast<uint16_t*>(ws + TL.a);
+  uint16_t* q = reinterpret_cast<uint16_t*>(ws + TL.q);
+  uint16_t* o = reinterpret_cast<uint16_t*>(ws + TL.o);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + TL.h);
+  float* acc = reinterpret_cast<float*>(ws + TL.acc);
+  float* x0 = (ex & NC_EXTRA_RESID_LAMBDAS) ? reinterpret_cast<float*>(ws + TL.x0) : nullptr;
+  float* xmid = (ex & NC_EXTRA_BACKOUT) ? reinterpret_cast<float*>(ws + TL.xmid) : nullptr;
+  const int mid = cfg->n_layer / 2;
+  const int C = cfg->d_model, D = cfg->head_dim, H = cfg->n_head, Hkv = cfg->n_kv_head, V = cfg->vocab;
+  const int NQKV = (H + 2 * Hkv) * D, M = B * N;
+  const bool f16 = cfg->act_dtype == NC_F16;
+  const float eps = cfg->norm_eps;
+  nc_status s;
+#define NC_TRY(call)    \
+  do {                  \
+    s = (call);         \
+    if (s != NC_OK) return s; \
+  } while (0)
+  if (cudaMemsetAsync(status, 0, 256, st) != cudaSuccess) return NC_ERR_CUDA;
+  NC_TRY(tree_mask_launch(parents, mask, B, N, st));
+  NC_TRY(tree_embedding_launch(tokens, parents, mask, lens, hist, w->wte, hist ? w->smear_gate : nullptr, x, x0, B, N,
+                               C, V, T_max, status, st));
+  // the projections as in a decode step: the skinny GEMM up to 32 rows, the
+  // tcgen05 GEMM with split K beyond
+  const bool skinny = M <= 32;
+  auto proj = [&](const uint16_t* in, int K, const uint16_t* wt, int n, float* out) -> nc_status {
+    if (skinny) return skinny_gemm_launch(in, K, wt, K, out, n, M, n, K, 0, 0.0f, f16, st);
+    EpiParams e{};
+    e.out = out;
+    e.ldo = n;
+    e.ksplit = resid_ksplit(M, n, K);
+    return gemm_launch(in, K, wt, K, M, n, K, EPI_RESID_F32, f16, e, status, st);
+  };
+  for (int l = 0; l < cfg->n_layer; ++l) {
+    float* keep = (xmid && l == mid) ? xmid : nullptr;
+    if (x0 || keep)
+      NC_TRY(rmsnorm_mix_launch(x, x0, x0 ? w->resid_lambdas + l : nullptr, x0 ? w->x0_lambdas + l : nullptr, keep,
+                                nullptr, nullptr, x0 != nullptr, a, M, C, eps, f16, st));
+    else
+      NC_TRY(rmsnorm_launch(x, a, M, C, eps, f16, st));
+    uint16_t* kvl = kv + l * TL.kv_layer_elems;
+    if (cudaMemsetAsync(acc, 0, (size_t)M * NQKV * 4, st) != cudaSuccess) return NC_ERR_CUDA;
+    NC_TRY(proj(a, C, wqkv + l * SL.wqkv_elems, NQKV, acc));
+    DecodeVe ve{};
+    if ((ex & NC_EXTRA_VALUE_EMBED) && nc_layer_value_embed(cfg, l) == 1)
+      ve = DecodeVe{tokens, w->value_embeds[l], w->ve_gates[l], V};
+    NC_TRY(tree_qkv_finish_launch(acc, mask, lens, q, kvl, rope, B, N, H, Hkv, D, T_max, eps, f16, status, ve, st));
+    NC_TRY(tree_attention_launch(q, (int64_t)H * D, kvl, cache + l * SL.cache_layer_elems, lens, mask, o, B, N, H,
+                                 Hkv, D, T_max, nc_layer_window(cfg, l), f16, st));
+    NC_TRY(proj(o, H * D, wo + l * SL.wo_elems, C, x));
+    NC_TRY(rmsnorm_launch(x, a, M, C, eps, f16, st));
+    if (cudaMemsetAsync(acc, 0, (size_t)M * 4 * C * 4, st) != cudaSuccess) return NC_ERR_CUDA;
+    NC_TRY(proj(a, C, wfc + l * SL.wfc_elems, 4 * C, acc));
+    NC_TRY(relu2_finish_launch(acc, h, (int64_t)M * 4 * C, f16, st, status));
+    NC_TRY(proj(h, 4 * C, wmp + l * SL.wmp_elems, C, x));
+  }
+  if (xmid)
+    NC_TRY(rmsnorm_mix_launch(x, nullptr, nullptr, nullptr, nullptr, xmid, w->backout_lambda, false, a, M, C, eps, f16,
+                              st));
+  else
+    NC_TRY(rmsnorm_launch(x, a, M, C, eps, f16, st));
+  if (skinny) {
+    NC_TRY(skinny_gemm_launch(a, C, wlm, C, logits, V, M, V, C, 2, cfg->softcap, f16, st));
+  } else {
+    EpiParams ep{};
+    ep.out = logits;
+    ep.ldo = V;
+    ep.cap = cfg->softcap;
+    NC_TRY(gemm_launch(a, C, wlm, C, M, V, C, EPI_SOFTCAP_F32, f16, ep, status, st));
+  }
+#undef NC_TRY
+  return NC_OK;
+}
+
+nc_status nc_accept_tree(const nc_config* cfg, const int32_t* tokens, const int32_t* parents, const int32_t* sampled,
+                         const int32_t* lens, int B, int N, int32_t* path, int32_t* count, int32_t* next,
+                         int32_t* lens_out, void* session, size_t session_bytes, int T_max, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  if (!cfg || !tokens || !parents || !sampled || !lens || !path || !count || !next || !lens_out || lens_out == lens ||
+      !session || !workspace)
+    return NC_ERR_INVALID_ARG;
+  if (nc_status s = tree_step_check(cfg, B, N, session, session_bytes, T_max, workspace, ws_bytes)) return s;
+  if (nc_status s = device_ok()) return s;
+  const SessionLayout SL = session_layout(cfg, B, T_max);
+  const TreeLayout TL = tree_layout(cfg, B, N);
+  uint8_t* base = static_cast<uint8_t*>(session);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* hist = (cfg->extras & NC_EXTRA_SMEAR) ? reinterpret_cast<int32_t*>(base + SL.hist) : nullptr;
+  return tree_accept_launch(tokens, parents, reinterpret_cast<const uint32_t*>(ws + TL.mask), sampled, lens,
+                            reinterpret_cast<const uint16_t*>(ws + TL.kv),
+                            reinterpret_cast<uint16_t*>(base + SL.cache), path, count, next, lens_out, hist, B, N,
+                            cfg->n_layer, T_max, 2 * cfg->n_kv_head * cfg->head_dim, S(stream));
+}
+
+}  // extern "C"
+
 namespace {
 
 // Workspace of nc_forward_backward.  Per layer l: the residual stream entering

@@ -249,6 +249,42 @@ nc_status decode_embedding_launch(const int32_t* tokens, int32_t* hist, const fl
 nc_status relu2_finish_launch(const float* acc, uint16_t* out, int64_t n, bool f16, cudaStream_t stream,
                               uint32_t* dev_status = nullptr);
 
+// ---- drafted trees (nc_tree.cu); see nc_decode_tree
+constexpr int kTreeMaxNodes = 128;
+nc_status tree_mask_launch(const int32_t* parents, uint32_t* mask, int B, int N, cudaStream_t stream);
+nc_status tree_attention_launch(const uint16_t* q, int64_t q_stride, const uint16_t* kv, const uint16_t* cache,
+                                const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H,
+                                int Hkv, int D, int T_max, int window, bool f16, cudaStream_t stream);
+// width: 16-bit elements of one position's k|v heads.  hist (or NULL): the
+// session's token record [B][T_max], where the accepted tokens go.
+nc_status tree_accept_launch(const int32_t* tokens, const int32_t* parents, const uint32_t* mask,
+                             const int32_t* sampled, const int32_t* lens, const uint16_t* kv, uint16_t* cache,
+                             int32_t* path, int32_t* count, int32_t* next, int32_t* lens_out, int32_t* hist, int B,
+                             int N, int L, int T_max, int width, cudaStream_t stream);
+// The token embedding of the nodes [B, N] with smear (smear_gate != NULL: the
+// previous token is the parent's, for a root the one recorded at lens[b] - 1)
+// and an optional copy into x0.  Unused nodes read row 0.
+nc_status tree_embedding_launch(const int32_t* tokens, const int32_t* parents, const uint32_t* mask,
+                                const int32_t* lens, const int32_t* hist, const float* wte, const float* smear_gate,
+                                float* x, float* x0, int B, int N, int C, int V, int T_max, uint32_t* dev_status,
+                                cudaStream_t stream);
+// From the fp32 sums of the nodes' QKV projection [B N, (H + 2 Hkv) D]: RoPE at
+// each node's position and QK-norm of q and k heads, q [B N, H, D] and the
+// drafted kv [B N, 2, Hkv, D] in 16 bits (ve as for qkv_finish_launch).
+nc_status tree_qkv_finish_launch(const float* acc, const uint32_t* mask, const int32_t* lens, uint16_t* q,
+                                 uint16_t* kv, const float* rope, int B, int N, int H, int Hkv, int D, int T_max,
+                                 float eps, bool f16, uint32_t* dev_status, DecodeVe ve, cudaStream_t stream);
+
+// ---- sampling (nc_sample.cu)
+nc_status sample_launch(const float* logits, int64_t ld, const float* u, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+                        float* logprob, int M, int V, cudaStream_t stream);
+
+// ---- distillation (nc_distill.cu); dz_kind: 0 none, 1 fp32, 2 bf16, 3 fp16
+nc_status distill_topk_launch(const float* z, const int32_t* idx, const float* teacher, const float* weight,
+                              float* loss, void* dz, int dz_kind, int M, int V, int K, float tau, float cap,
+                              uint32_t* dev_status, cudaStream_t stream);
+
 nc_status rmsnorm_launch(const float* x, uint16_t* out, int M, int C, float eps, bool f16,
                          cudaStream_t stream,
                          float* amax = nullptr);

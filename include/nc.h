@@ -280,6 +280,44 @@ nc_status nc_decode_step_dev(const nc_config* cfg, const nc_weights* w, const in
                              int32_t* pos_dev, float* logits, void* session, size_t session_bytes, int T_max,
                              void* stream);
 
+/* ---- a tree of drafted tokens over the session (speculative decoding)
+ * Each row b has its own committed length lens[b] (device int32): positions
+ * [0, lens[b]) of its cache are filled.  A step takes N <= 128 drafted tokens a
+ * row as a tree: parents[b][i] < i is the index of node i's parent, -1 for a
+ * root, -2 (or anything else outside [-1, i)) for an unused node (padding of a
+ * row whose tree is smaller).  Node 0 is the row's next token; a node sits at
+ * position lens[b] + its depth.  nc_decode_tree gives the logits of every node,
+ * the caller samples a token at every node (nc_sample over the B * N rows), and
+ * nc_accept_tree finds the path that the samples confirm and moves its keys and
+ * values into the cache.  N = 1 is a decode step whose rows have lengths of
+ * their own.  The session is nc_prefill's (cfg->fp8 must be 0); any
+ * n_head / n_kv_head is taken. */
+
+/* Bytes of the workspace of nc_decode_tree / nc_accept_tree (0 on bad input).
+ * Host only. */
+size_t nc_tree_workspace_bytes(const nc_config* cfg, int B, int N);
+
+/* Logits [B, N, V] (fp32, device, 16-byte aligned) of the drafted tokens
+ * [B, N]: soft-capped, equal at each node to those of nc_forward over the row's
+ * prefix followed by the node's path.  The drafted keys and values and the
+ * ancestor words stay in the workspace (nc_tree_workspace_bytes(cfg, B, N)
+ * bytes, 256-byte aligned) for nc_accept_tree; the cache is only read.  A node
+ * whose position is T_max or more, and an unused one, gets meaningless logits.
+ * lens is clamped to [0, T_max].  The status word of the session is cleared and
+ * gets the conditions of nc_decode_step (a token id of an unused node is not
+ * looked at).  Nothing is read on the host: the step can be captured. */
+nc_status nc_decode_tree(const nc_config* cfg, const nc_weights* w, const int32_t* tokens, const int32_t* parents,
+                         const int32_t* lens, int B, int N, float* logits, void* session, size_t session_bytes,
+                         int T_max, void* workspace, size_t ws_bytes, void* stream);
+
+/* nc_tree_accept over every layer of the session, after nc_decode_tree of the
+ * same tokens, parents, lens and workspace; with NC_EXTRA_SMEAR the accepted
+ * tokens are recorded too.  sampled [B, N]: the token sampled at each node. */
+nc_status nc_accept_tree(const nc_config* cfg, const int32_t* tokens, const int32_t* parents, const int32_t* sampled,
+                         const int32_t* lens, int B, int N, int32_t* path, int32_t* count, int32_t* next,
+                         int32_t* lens_out, void* session, size_t session_bytes, int T_max, void* workspace,
+                         size_t ws_bytes, void* stream);
+
 /* Kinds of kernel launch reported by nc_forward_traced. */
 typedef enum {
   NC_K_ROPE_TABLE = 0,
@@ -575,6 +613,90 @@ nc_status nc_lm_head_loss_static(const uint16_t* a, const uint16_t* w_lm, const 
                                  int M, int C, int V, float cap, nc_dtype dtype,
                                  float* token_loss, float* loss, uint32_t* dev_status,
                                  void* stream);
+
+/* ---------------------------------------------------------------- drafted trees
+ * Each step of the tree path on its own (see nc_decode_tree).  int32 and fp32
+ * arrays need no more than their natural alignment; 16-bit tensors 16 bytes. */
+
+/* mask [B, N, ceil(N / 32)] from parents [B, N] (1 <= N <= 128): bit j % 32 of
+ * word j / 32 of node i is set where j is i or an ancestor of i.  A node whose
+ * walk up leaves [0, i) before it ends at a root (-1) is unused: all bits 0. */
+nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, void* stream);
+
+/* Attention of the N drafted nodes of every row over the cache and their own
+ * ancestors: node i (depth_i = bits of mask_i - 1, position lens[b] + depth_i)
+ *   out[b,i,h,:] = sum_j softmax_j(q[b,i,h,:] . k_j / sqrt(D)) v_j
+ * over the committed keys t < lens[b] with lens[b] + depth_i - t < window and
+ * the drafted keys j in mask_i with depth_i - depth_j < window (window <= 0:
+ * all).  A node whose own bit is clear is unused: output 0, and its drafted K/V
+ * are not read.  q: node n of row b at q + (b N + n) q_row_stride, H heads of D
+ * (q_row_stride >= H D, a multiple of 8); kv [B, N, 2, Hkv, D]; cache
+ * [B, T_max, 2, Hkv, D]; out [B, N, H, D]; 16-bit in format dtype.  lens [B] is
+ * clamped to [0, T_max]; positions at and past it are not read.  D in {64,
+ * 128}, 1 <= N <= 128, B <= 65535, H <= 4096.  K and V of committed positions
+ * inside the root's window and of used nodes must be finite.  One launch, no
+ * workspace, the same result run to run. */
+nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
+                            const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
+                            int D, int T_max, int window, nc_dtype dtype, void* stream);
+
+/* The accepted path of each row's tree, and its K/V moved into the cache: the
+ * path starts at node 0 (if it is used) and goes on from node a to its first
+ * child (parents[c] == a, c > a, used) with tokens[c] == sampled[a], while the
+ * position lens[b] + (nodes so far) is below T_max.
+ *   path [B, N] the accepted nodes, then -1; count [B]; next [B] the token
+ *   sampled at the last accepted node (tokens[b][0] when count is 0);
+ *   lens_out [B] = lens (clamped to [0, T_max]) + count;
+ *   cache[l, b, lens[b] + k] = kv[l, b, path[b][k]] for every layer l < L.
+ * kv [L, B, N, 2, Hkv, D], cache [L, B, T_max, 2, Hkv, D] 16-bit; mask as
+ * nc_tree_mask writes it.  lens_out may not be lens.  1 <= N <= 128,
+ * 1 <= L <= 65535, Hkv D a multiple of 4.  One launch. */
+nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const uint32_t* mask, const int32_t* sampled,
+                         const int32_t* lens, const uint16_t* kv, uint16_t* cache, int32_t* path, int32_t* count,
+                         int32_t* next, int32_t* lens_out, int B, int N, int L, int Hkv, int D, int T_max,
+                         void* stream);
+
+/* One token a row from logits (M rows of V fp32, row_stride >= V elements
+ * apart) and given uniform numbers u [M] in [0, 1):
+ *   w_i = exp((l_i - max l) / T); order: logit descending, index ascending;
+ *   kept: the first top_k; of these the shortest prefix whose mass reaches
+ *   top_p of theirs (at least one token); of these the ones with w_i >= min_p;
+ *   tokens[m] = the first kept index, in index order, whose running mass
+ *   exceeds u times the kept mass; logprob[m] = log(w_token / kept mass).
+ * temperature, top_p, min_p [M] fp32 and top_k [M] int32 are each NULL (1, off,
+ * off, off) or per row: temperature <= 0 (or NaN) takes the largest logit
+ * (lowest index; logprob 0); top_k <= 0, top_p >= 1 and min_p <= 0 (or NaN) are
+ * off; top_p <= 0 (or NaN) and min_p >= 1 keep the largest logits only.  u is
+ * clamped to [0, 1] (NaN: 0); 1 takes the last kept token.  NaN logits count as
+ * -inf, which is never sampled; a row of those alone gives token -1 and logprob
+ * -inf.  logprob may be NULL.  Weights are exact to 2^-47 or better at V <=
+ * 32768 (an absolute unit of V / 2^62; smaller weights count as 0) and sums are
+ * exact, so the result is the same run to run.  1 <= V <= 2^24. */
+nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, float* logprob,
+                    int M, int V, void* stream);
+
+/* Element types of a logit gradient. */
+typedef enum { NC_GRAD_BF16 = 0, NC_GRAD_F16 = 1, NC_GRAD_F32 = 2, NC_GRAD_NONE = 3 } nc_grad_dtype;
+
+/* Distillation from the K largest logits of a teacher (the draft model's
+ * training loss), stands beside nc_softcap_ce:
+ *   l = cap tanh(z / cap) (cap = 0: l = z), p = softmax(l / tau) over V,
+ *   q = softmax(t / tau) over the row's teacher entries,
+ *   token_loss = tau^2 sum_k q_k (log q_k - log p_{idx_k}),
+ *   dz_i = row_weight tau (p_i - sum_{idx_k = i} q_k) (1 - (l_i / cap)^2),
+ * dz being the gradient of row_weight * token_loss with respect to z.
+ * z [M, V] fp32, teacher_idx [M, K] int32, teacher_logits [M, K] fp32 (after
+ * the teacher's own soft-cap), row_weight [M] fp32 or NULL (1), token_loss [M]
+ * fp32, dz [M, V] in dz_dtype or NULL (with NC_GRAD_NONE).  An entry with index
+ * -1 or logit -inf is unused; an index outside [-1, V) is unused and sets
+ * NC_DEV_TARGET_RANGE; an index may occur more than once.  A row with no entry
+ * has loss 0 and gradient 0.  fp16 gradients saturate at +-65504.  tau > 0,
+ * cap >= 0, 1 <= K <= 1024, 1 <= V.  z needs a finite maximum in each row.  dz
+ * may not overlap z.  Same result run to run. */
+nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const float* teacher_logits,
+                          const float* row_weight, float* token_loss, void* dz, nc_grad_dtype dz_dtype, int M, int V,
+                          int K, float tau, float cap, uint32_t* dev_status, void* stream);
 
 /* Self-test of the failure path of in-kernel waits: one CTA waits on an
  * mbarrier that nothing arrives on, through the same bounded wait the GEMM

@@ -160,7 +160,9 @@ def lib():
                                      vp]),
             "nc_accept_tree": (i32, [cfgp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, i32, vp, sz, vp]),
             "nc_tree_mask": (i32, [vp, vp, i32, i32, vp]),
-            "nc_tree_attention": (i32, [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]),
+            "nc_tree_attention": (i32, [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, sz,
+                                        vp]),
+            "nc_tree_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
             "nc_tree_accept": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
             "nc_sample": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp]),
             "nc_distill_topk": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp]),
@@ -791,13 +793,14 @@ def tree_mask(parents, mask, stream=None):
     _launch(where, dev, stream, lib().nc_tree_mask, *a, B, N)
 
 
-def tree_attention(q, kv, cache, lens, mask, out, window=0, stream=None):
+def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stream=None):
     """Attention of the drafted nodes of every row over the cache and their
     ancestors (nc_tree_attention).
 
     q [B, N, H, D] (the nodes may be strided), kv [B, N, 2, Hkv, D], cache
     [B, T_max, 2, Hkv, D], out [B, N, H, D]: fp16 or bf16; lens [B] int32, mask
-    [B, N, ceil(N / 32)] int32 (tree_mask)."""
+    [B, N, ceil(N / 32)] int32 (tree_mask).  workspace: a uint8 tensor of
+    nc_tree_attention_workspace_bytes bytes (None: a new one)."""
     import torch
     where = "tree_attention"
     if q.dim() != 4 or cache.dim() != 5:
@@ -814,9 +817,17 @@ def tree_attention(q, kv, cache, lens, mask, out, window=0, stream=None):
          _arg(where, "lens", lens, torch.int32, (B,), dev),
          _arg(where, "mask", mask, torch.int32, (B, N, (N + 31) // 32), dev),
          _arg(where, "out", out, dt, (B, N, H, D), dev))
-    if B:
-        _launch(where, dev, stream, lib().nc_tree_attention, q.data_ptr(), qs, *a, B, N, H, Hkv, D, T_max, window,
-                _dt(q))
+    if B == 0:
+        return
+    need = lib().nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, window)
+    if workspace is None and need and dev.type == "cuda":
+        with _allocate_on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if workspace is not None and workspace.device != dev:
+        raise NcError(1, f"{where}: the workspace is on {workspace.device}, expected {dev}")
+    _launch(where, dev, stream, lib().nc_tree_attention, q.data_ptr(), qs, *a, B, N, H, Hkv, D, T_max, window, _dt(q),
+            wp, wn)
 
 
 def sample(logits, u, tokens, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):

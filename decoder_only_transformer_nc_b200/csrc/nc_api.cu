@@ -1102,17 +1102,28 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
   return tree_mask_launch(parents, mask, B, N, S(stream));
 }
 
+size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int window) {
+  if (B < 1 || B > 65535 || N < 1 || N > kTreeMaxNodes || H < 1 || H > 4096 || Hkv < 1 || H % Hkv != 0 ||
+      (D != 64 && D != 128))
+    return 0;
+  return tree_attention_bytes(B, N, H, Hkv, D, window);
+}
+
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
                             const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
-                            int D, int T_max, int window, nc_dtype dtype, void* stream) {
+                            int D, int T_max, int window, nc_dtype dtype, void* workspace, size_t ws_bytes,
+                            void* stream) {
   if (!q || !kv || !cache || !lens || !mask || !out || B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || !dtype_ok(dtype))
     return NC_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || N < 1 || N > kTreeMaxNodes || T_max < 1 || B > 65535 || H > 4096) return NC_ERR_SHAPE;
   if (q_row_stride < (int64_t)H * D || q_row_stride % 8) return NC_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(kv) || !aligned16(cache) || !aligned16(out)) return NC_ERR_ALIGNMENT;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace))
+    return NC_ERR_ALIGNMENT;
+  const size_t need = tree_attention_bytes(B, N, H, Hkv, D, window);
+  if (need > 0 && (!workspace || ws_bytes < need)) return NC_ERR_WORKSPACE;
   if (nc_status s = device_ok()) return s;
   return tree_attention_launch(q, q_row_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window,
-                               dtype == NC_F16, S(stream));
+                               dtype == NC_F16, workspace, nullptr, S(stream));
 }
 
 nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const uint32_t* mask, const int32_t* sampled,
@@ -1163,7 +1174,7 @@ namespace {
 // layer's drafted K/V [B][N][2][Hkv][D] (kept for the acceptance) and the
 // step's activations for B N rows.  Offsets are 256-byte aligned.
 struct TreeLayout {
-  size_t mask, kv, x, a, q, o, h, acc, x0, xmid, total;
+  size_t mask, kv, x, a, q, o, h, acc, attn, x0, xmid, total;
   size_t kv_layer_elems;
 };
 
@@ -1186,6 +1197,9 @@ TreeLayout tree_layout(const nc_config* c, int B, int N) {
   L.o = take(M * H * D * 2);
   L.h = take(M * 4 * C * 2);
   L.acc = take(M * (nqkv > 4 * C ? nqkv : 4 * C) * 4);
+  // every layer has one of the two windows
+  L.attn = take(std::max(tree_attention_bytes(B, N, c->n_head, c->n_kv_head, c->head_dim, 0),
+                         tree_attention_bytes(B, N, c->n_head, c->n_kv_head, c->head_dim, c->short_window)));
   L.x0 = (c->extras & NC_EXTRA_RESID_LAMBDAS) ? take(M * C * 4) : 0;
   L.xmid = (c->extras & NC_EXTRA_BACKOUT) ? take(M * C * 4) : 0;
   L.total = off;
@@ -1292,7 +1306,7 @@ nc_status nc_decode_tree(const nc_config* cfg, const nc_weights* w, const int32_
       ve = DecodeVe{tokens, w->value_embeds[l], w->ve_gates[l], V};
     NC_TRY(tree_qkv_finish_launch(acc, mask, lens, q, kvl, rope, B, N, H, Hkv, D, T_max, eps, f16, status, ve, st));
     NC_TRY(tree_attention_launch(q, (int64_t)H * D, kvl, cache + l * SL.cache_layer_elems, lens, mask, o, B, N, H,
-                                 Hkv, D, T_max, nc_layer_window(cfg, l), f16, st));
+                                 Hkv, D, T_max, nc_layer_window(cfg, l), f16, ws + TL.attn, status, st));
     NC_TRY(proj(o, H * D, wo + l * SL.wo_elems, C, x));
     NC_TRY(rmsnorm_launch(x, a, M, C, eps, f16, st));
     if (cudaMemsetAsync(acc, 0, (size_t)M * 4 * C * 4, st) != cudaSuccess) return NC_ERR_CUDA;

@@ -254,7 +254,17 @@ constexpr int kTreeMaxNodes = 128;
 nc_status tree_mask_launch(const int32_t* parents, uint32_t* mask, int B, int N, cudaStream_t stream);
 nc_status tree_attention_launch(const uint16_t* q, int64_t q_stride, const uint16_t* kv, const uint16_t* cache,
                                 const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H,
-                                int Hkv, int D, int T_max, int window, bool f16, cudaStream_t stream);
+                                int Hkv, int D, int T_max, int window, bool f16, void* workspace,
+                                uint32_t* dev_status, cudaStream_t stream);
+// Workspace bytes of tree_attention_launch (0: none is used).
+size_t tree_attention_bytes(int B, int N, int H, int Hkv, int D, int window);
+// The tcgen05 kernel of the same attention (nc_tree_tc.cu), for the sizes that fit it.
+bool tree_attention_tc_fits(int B, int N, int H, int Hkv, int window);
+size_t tree_attention_tc_bytes(int D);
+nc_status tree_attention_tc_launch(const uint16_t* q, int64_t q_stride, const uint16_t* kv, const uint16_t* cache,
+                                   const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H,
+                                   int Hkv, int D, int T_max, int window, bool f16, void* workspace,
+                                   uint32_t* dev_status, cudaStream_t stream);
 // width: 16-bit elements of one position's k|v heads.  hist (or NULL): the
 // session's token record [B][T_max], where the accepted tokens go.
 nc_status tree_accept_launch(const int32_t* tokens, const int32_t* parents, const uint32_t* mask,

@@ -615,10 +615,23 @@ nc_status tree_mask_launch(const int32_t* parents, uint32_t* mask, int B, int N,
   return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
 }
 
+// Rows of a kv group beyond which the tcgen05 kernel takes over.
+static bool use_tc(int B, int N, int H, int Hkv, int window) {
+  return N * (H / Hkv) > 32 && tree_attention_tc_fits(B, N, H, Hkv, window);
+}
+
+size_t tree_attention_bytes(int B, int N, int H, int Hkv, int D, int window) {
+  return use_tc(B, N, H, Hkv, window) ? tree_attention_tc_bytes(D) : 0;
+}
+
 nc_status tree_attention_launch(const uint16_t* q, int64_t q_stride, const uint16_t* kv, const uint16_t* cache,
                                 const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H,
-                                int Hkv, int D, int T_max, int window, bool f16, cudaStream_t stream) {
+                                int Hkv, int D, int T_max, int window, bool f16, void* workspace,
+                                uint32_t* dev_status, cudaStream_t stream) {
   if (B == 0) return NC_OK;
+  if (use_tc(B, N, H, Hkv, window))
+    return tree_attention_tc_launch(q, q_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window, f16,
+                                    workspace, dev_status, stream);
   const TreeAttnParams p{q, q_stride, kv, cache, lens, mask, out, N, H, Hkv, T_max, window,
                          1.4426950408889634f / sqrtf((float)D)};
   if (D == 128) return f16 ? tree_attn_rows<128, true>(p, B, stream) : tree_attn_rows<128, false>(p, B, stream);

@@ -634,11 +634,15 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * [B, T_max, 2, Hkv, D]; out [B, N, H, D]; 16-bit in format dtype.  lens [B] is
  * clamped to [0, T_max]; positions at and past it are not read.  D in {64,
  * 128}, 1 <= N <= 128, B <= 65535, H <= 4096.  K and V of committed positions
- * inside the root's window and of used nodes must be finite.  One launch, no
- * workspace, the same result run to run. */
+ * inside the root's window and of used nodes must be finite.  workspace: at
+ * least nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where
+ * that is 0); calls that overlap in time need one each.  The result is the same
+ * run to run. */
+size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int window);
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
                             const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
-                            int D, int T_max, int window, nc_dtype dtype, void* stream);
+                            int D, int T_max, int window, nc_dtype dtype, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 /* The accepted path of each row's tree, and its K/V moved into the cache: the
  * path starts at node 0 (if it is used) and goes on from node a to its first

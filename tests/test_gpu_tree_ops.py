@@ -90,6 +90,15 @@ ATTN = [
     (1, 128, 3, 1, 128, 50, [50], 0, "fp16", "random"),    # three heads a group
     (4, 100, 8, 1, 64, 33, [0, 1, 32, 33], 1, "bf16", "ragged"),  # a window of one: a node sees itself
     (2, 17, 5, 5, 128, 1500, [1411, 1500], 0, "bf16", "ragged"),
+    # more rows a kv head than the small kernel takes
+    (7, 40, 2, 2, 128, 400, [0, 1, 127, 128, 129, 399, 400], 0, "fp16", "random"),
+    (7, 33, 2, 1, 64, 400, [0, 1, 127, 128, 129, 399, 400], 0, "bf16", "ragged"),
+    (3, 64, 8, 2, 128, 600, [600, 5, 257], 0, "bf16", "ragged"),    # two row tiles a unit
+    (2, 100, 3, 1, 64, 500, [500, 333], 129, "fp16", "forest"),     # three row tiles of 42 nodes
+    (1, 64, 4, 1, 128, 3000, [2999], 0, "fp16", "random"),          # one unit over every SM
+    (5, 128, 4, 4, 64, 300, [300, 299, 0, 150, 1], 200, "fp16", "chain"),
+    (1, 3, 128, 1, 64, 260, [260], 0, "bf16", "random"),            # 128 heads a group
+    (1, 2, 200, 1, 64, 130, [130], 0, "bf16", "random"),            # more heads a group than a tile has rows
 ]
 
 
@@ -106,17 +115,19 @@ def test_tree_attention(gpu, case):
 
 
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
-def test_tree_attention_reads_nothing_unseen(gpu, dt):
+@pytest.mark.parametrize("H,W", [(4, 40), (16, 0), (16, 140), (8, 0)])
+def test_tree_attention_reads_nothing_unseen(gpu, dt, H, W):
     """NaN behind a row's length, before the window, in unused nodes' q, K and V; lengths out
     of range are clamped; a strided q."""
-    B, N, H, Hkv, D, T, W = 3, 21, 4, 2, 64, 150, 40
-    q, kv, cache, lens, mask = _attn_case(5, B, N, H, Hkv, D, T, [150, 77, 0], dt, "ragged")
+    B, N, Hkv, D, T = 3, 21, 2, 64, 350
+    q, kv, cache, lens, mask = _attn_case(5, B, N, H, Hkv, D, T, [350, 77, 0], dt, "ragged")
     mask[0] = o64.tree_mask(_trees(np.random.default_rng(1), 1, N, "random"))[0]
     mask[1, 9:] = 0
     clean = (kv.clone(), cache.clone(), q.clone())
     for b in range(B):
         cache[b, lens[b]:] = math.nan
-        cache[b, :max(0, lens[b] - W + 1)] = math.nan
+        if W:
+            cache[b, :max(0, lens[b] - W + 1)] = math.nan
         for i in range(N):
             if not (mask[b, i, 0] >> i) & 1:
                 kv[b, i] = math.nan

@@ -30,15 +30,17 @@ def _code(nclib, fn, *a, **k):
 A = 1 << 40  # an aligned address that no check dereferences
 
 
-def _c_attn(nc, q=A, qs=512, kv=A, cache=A, lens=A, mask=A, out=A, B=1, N=4, H=4, Hkv=2, D=128, T=64, win=0, dt=1):
-    return nc.lib().nc_tree_attention(q, qs, kv, cache, lens, mask, out, B, N, H, Hkv, D, T, win, dt, None)
+def _c_attn(nc, q=A, qs=512, kv=A, cache=A, lens=A, mask=A, out=A, B=1, N=4, H=4, Hkv=2, D=128, T=64, win=0, dt=1, ws=None,
+            wn=0):
+    return nc.lib().nc_tree_attention(q, qs, kv, cache, lens, mask, out, B, N, H, Hkv, D, T, win, dt, ws, wn, None)
 
 
 def test_tree_attention_refusals(nclib):
     for bad, want in [(dict(q=None), 1), (dict(mask=None), 1), (dict(Hkv=3), 1), (dict(dt=2), 1), (dict(B=-1), 1),
                       (dict(D=96, qs=384), 3), (dict(N=0), 3), (dict(N=129), 3), (dict(T=0), 3), (dict(B=65536), 3),
                       (dict(qs=504), 1), (dict(qs=513), 1), (dict(q=A + 2), 4), (dict(kv=A + 8), 4),
-                      (dict(cache=A + 4), 4), (dict(out=A + 2), 4)]:
+                      (dict(cache=A + 4), 4), (dict(out=A + 2), 4), (dict(ws=A + 8), 4),
+                      (dict(N=64, ws=None), 5), (dict(N=64, ws=A, wn=1000), 5)]:
         assert _c_attn(nclib, **bad) == want, bad
     good = dict(q=_h(2, 3, 4, 64), kv=_h(2, 3, 2, 2, 64), cache=_h(2, 9, 2, 2, 64), lens=_i(2), mask=_i(2, 3, 1),
                 out=_h(2, 3, 4, 64))

@@ -1115,7 +1115,9 @@ nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint1
                             void* stream) {
   if (!q || !kv || !cache || !lens || !mask || !out || B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || !dtype_ok(dtype))
     return NC_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || N < 1 || N > kTreeMaxNodes || T_max < 1 || B > 65535 || H > 4096) return NC_ERR_SHAPE;
+  if ((D != 64 && D != 128) || N < 1 || N > kTreeMaxNodes || T_max < 1 || T_max > (1 << 22) ||
+      B > 65535 || H > 4096)
+    return NC_ERR_SHAPE;
   if (q_row_stride < (int64_t)H * D || q_row_stride % 8) return NC_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace))
     return NC_ERR_ALIGNMENT;
@@ -1213,7 +1215,8 @@ bool tree_shape_ok(int B, int N) {
 nc_status tree_step_check(const nc_config* cfg, int B, int N, const void* session, size_t session_bytes, int T_max,
                           const void* workspace, size_t ws_bytes) {
   if (!config_ok(cfg) || cfg->fp8 != 0) return NC_ERR_CONFIG;
-  if (!tree_shape_ok(B, N) || T_max < 1 || T_max > cfg->seq_len || cfg->n_head > 4096) return NC_ERR_SHAPE;
+  if (!tree_shape_ok(B, N) || T_max < 1 || T_max > cfg->seq_len || T_max > (1 << 22) || cfg->n_head > 4096)
+    return NC_ERR_SHAPE;
   if (session_bytes < session_layout(cfg, B, T_max).total || ws_bytes < tree_layout(cfg, B, N).total)
     return NC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(session) & 255u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

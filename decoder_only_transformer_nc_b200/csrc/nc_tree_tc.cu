@@ -57,7 +57,7 @@ struct Geo {
   static constexpr int OFF_BAR = OFF_V + 2 * TILE;
   static constexpr int OFF_X = OFF_BAR + 256;   // (max, sum) of both streams, by piece parity [2][2][128][2]
   static constexpr int OFF_PRE = OFF_X + 2 * 2 * 128 * 2 * 4;
-  static constexpr int SMEM_BYTES = OFF_PRE + (kMaxB + 1) * 8;
+  static constexpr int SMEM_BYTES = OFF_PRE + (2 * kMaxB + 1) * 4;
 };
 
 struct Bars {
@@ -76,7 +76,7 @@ struct Params {
   const int32_t* lens;
   const uint32_t* mask;
   uint16_t* out;
-  float* part;  // [CTAs][2][256][D] then [CTAs][2][256][2]
+  float* part;  // [CTAs][2 pieces][2 row tiles][D + 2][128]: O, max, sum; rows innermost
   int B, N, H, Hkv, T_max, win;
   int G, npt, tiles_r, pairs;  // query heads a kv head, nodes a row tile, row tiles, pairs of them
   float scale_log2;
@@ -88,48 +88,67 @@ struct Row {  // one cache row's committed keys
   int len, lo, n_c;
 };
 
-__device__ __forceinline__ Row row_of(const Params& p, int b) {
+__device__ __forceinline__ Row row_of(const Params& p, int len) {
   Row r;
-  r.len = min(max(p.lens[b], 0), p.T_max);
-  r.lo = max(0, r.len - p.win + 1);
+  r.len = len;
+  r.lo = max(0, len - p.win + 1);
   r.n_c = (r.len - r.lo + BKV - 1) / BKV;
   return r;
 }
 
-// pre[b] = tiles of one unit summed over the rows before b (times the units of
-// a row: the linear tile index of row b's first tile); pre[B] = all tiles.
-__device__ __forceinline__ void fill_prefix(const Params& p, int64_t* pre) {
+// The work in shared memory: pre[b] = linear index of row b's first tile (its
+// units one after another), pre[B] = all tiles, len[b] = the clamped lengths.
+// (Fewer than 2^31 tiles: see tree_attention_tc_fits.)
+struct Plan {
+  int* pre;
+  int* len;
+};
+
+__device__ __forceinline__ Plan make_plan(const Params& p, int* mem) {
+  const Plan pl{mem, mem + p.B + 1};
   const int upr = p.Hkv * p.pairs;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) pre[b + 1] = (int64_t)(row_of(p, b).n_c + 1) * upr;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int len = min(max(p.lens[b], 0), p.T_max);
+    pl.len[b] = len;
+    pl.pre[b + 1] = (row_of(p, len).n_c + 1) * upr;
+  }
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    int64_t run = 0;
+    int run = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int64_t v = b0 + lane < p.B ? pre[b0 + lane + 1] : 0;
+      int v = b0 + lane < p.B ? pl.pre[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += t;
       }
-      if (b0 + lane < p.B) pre[b0 + lane + 1] = run + v;
+      if (b0 + lane < p.B) pl.pre[b0 + lane + 1] = run + v;
       run += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) pre[0] = 0;
+    if (lane == 0) pl.pre[0] = 0;
   }
   __syncthreads();
+  return pl;
 }
+
+// First tile of CTA c: the tiles are dealt as evenly as they go.
+struct Deal {
+  int q, r;
+  __device__ Deal(int total, int ctas) : q(total / ctas), r(total % ctas) {}
+  __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
+};
 
 struct Seg {
   int b, g, pair;  // the unit
   int t0, n;       // its tiles [t0, t0 + n) ...
   int units_t;     // ... of this many
   bool two;        // two row tiles (streams share the key tiles)
-  int64_t u0;      // linear index of the unit's first tile
+  int u0;          // linear index of the unit's first tile
 };
 
 // The piece of work at linear tile x (< end).
-__device__ __forceinline__ Seg seg_at(const Params& p, const int64_t* pre, int64_t x, int64_t end) {
+__device__ __forceinline__ Seg seg_at(const Params& p, const int* pre, int x, int end) {
   int lo = 0, hi = p.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -141,24 +160,75 @@ __device__ __forceinline__ Seg seg_at(const Params& p, const int64_t* pre, int64
   const int upr = p.Hkv * p.pairs;
   Seg s;
   s.b = lo;
-  s.units_t = (int)((pre[lo + 1] - pre[lo]) / upr);
-  const int64_t rem = x - pre[lo];
-  const int u = (int)(rem / s.units_t);
-  s.t0 = (int)(rem - (int64_t)u * s.units_t);
+  s.units_t = (pre[lo + 1] - pre[lo]) / upr;
+  const int rem = x - pre[lo], u = rem / s.units_t;
+  s.t0 = rem - u * s.units_t;
   s.pair = u % p.pairs;
   s.g = u / p.pairs;
-  s.n = (int)min((int64_t)(s.units_t - s.t0), end - x);
+  s.n = min(s.units_t - s.t0, end - x);
   s.two = 2 * s.pair + 1 < p.tiles_r;
   s.u0 = x - s.t0;
   return s;
 }
 
-__device__ __forceinline__ int64_t cta_begin(int64_t total, int c, int n) { return total * c / n; }
-
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(got));
+  return got != 0;
+}
+
+// A matrix descriptor from its low word: the high word (stride 1024, version,
+// swizzle) is the same for all tiles here.  The issuing thread is one of a warp
+// that works alone, so the few instructions a descriptor costs count: an MMA of
+// 128 x 128 x 16 lasts 64 cycles.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "n"(hi));
+  return r;
+}
+
+// 32 lanes x 16 consecutive columns: thread i writes lane (base lane + i).
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32"
+      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  return pack_u32x2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 template <int D, bool F16>
@@ -179,7 +249,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* sm = smem_raw;
   Bars* bar = reinterpret_cast<Bars*>(sm + G::OFF_BAR);
   float* xval = reinterpret_cast<float*>(sm + G::OFF_X);
-  int64_t* pre = reinterpret_cast<int64_t*>(sm + G::OFF_PRE);
   const uint32_t s_q = smem_u32(sm), s_k = s_q + G::OFF_K, s_v = s_q + G::OFF_V;
   const uint32_t warp = warp_id_sync();
   const uint32_t lane = lane_id();
@@ -212,12 +281,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  fill_prefix(p, pre);  // ends with __syncthreads
+  const Plan pl = make_plan(p, reinterpret_cast<int*>(sm + G::OFF_PRE));  // ends with __syncthreads
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   const WaitCtl ctl{&bar->abort_flag, p.dev_status, p.limit_ns};
-  const int64_t total = pre[p.B];
-  const int64_t x_begin = cta_begin(total, blockIdx.x, gridDim.x), x_end = cta_begin(total, blockIdx.x + 1, gridDim.x);
+  const Deal deal(pl.pre[p.B], gridDim.x);
+  const int x_begin = deal.begin(blockIdx.x), x_end = deal.begin(blockIdx.x + 1);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -225,9 +294,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t outstanding = 0, out_phase = 0;  // bits 0,1: K slots; 2: Q; 3,4: V slots
       int gt = 0, n = 0;                        // tiles and pieces done before
       bool ok = true;
-      for (int64_t x = x_begin; x < x_end && ok; ++n) {
-        const Seg sg = seg_at(p, pre, x, x_end);
-        const Row rw = row_of(p, sg.b);
+      for (int x = x_begin; x < x_end && ok; ++n) {
+        const Seg sg = seg_at(p, pl.pre, x, x_end);
+        const Row rw = row_of(p, pl.len[sg.b]);
         if (!mbar_wait(smem_u32(&bar->q_empty), (n & 1) ^ 1, ctl)) break;
         const int nq = sg.two ? 2 : 1;
         const uint32_t qbytes = (uint32_t)(p.G * p.npt) * 128u * G::KA;
@@ -277,68 +346,74 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer
-      int gt = 0, n = 0;
-      int gp[2] = {0, 0};  // P V products issued for each stream
-      bool ok = true;
-      for (int64_t x = x_begin; x < x_end && ok; ++n) {
-        const Seg sg = seg_at(p, pre, x, x_end);
-        if (!mbar_wait(smem_u32(&bar->q_full), n & 1, ctl)) break;
-        tc_fence_after();
-        const int steps = sg.two ? sg.n : (sg.n + 1) / 2;
-        bool freed = n == 0;
-        for (int i = 0; i <= steps && ok; ++i) {
-          for (int w = 0; w < 2 && ok; ++w) {
-            const int tp = sg.two ? i - 1 : 2 * (i - 1) + w;  // tile of PV_w(i - 1)
-            if (i > 0 && tp < sg.n) {
-              const int gi = gt + tp, st = gi & 1;
-              if (!mbar_wait(smem_u32(&bar->v_full[st]), (uint32_t)(gi >> 1) & 1, ctl) ||
-                  !mbar_wait(smem_u32(&bar->p_full[w]), (uint32_t)gp[w] & 1, ctl) ||
-                  (!freed && !mbar_wait(smem_u32(&bar->o_free), (uint32_t)(n - 1) & 1, ctl))) {
-                ok = false;
-                break;
-              }
-              freed = true;
-              ++gp[w];
-              tc_fence_after();
-              const uint32_t vbase = s_v + st * G::TILE;
+    // ---------------- MMA issuer.  The whole warp walks the loop, one lane issues:
+    // the operands stay warp-uniform.
+    int gt = 0, n = 0;
+    int gp[2] = {0, 0};  // P V products issued for each stream
+    bool ok = true;
+    for (int x = x_begin; x < x_end && ok; ++n) {
+      const Seg sg = seg_at(p, pl.pre, x, x_end);
+      const int sn = __shfl_sync(0xffffffffu, sg.n, 0);
+      const bool two = __shfl_sync(0xffffffffu, (int)sg.two, 0) != 0;
+      if (!mbar_wait(smem_u32(&bar->q_full), n & 1, ctl)) break;
+      tc_fence_after();
+      const int steps = two ? sn : (sn + 1) / 2;
+      bool freed = n == 0;
+      for (int i = 0; i <= steps && ok; ++i) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int tp = two ? i - 1 : 2 * (i - 1) + w;  // tile of PV_w(i - 1)
+          if (ok && i > 0 && tp < sn) {
+            const int gi = gt + tp, st = gi & 1;
+            ok = mbar_wait(smem_u32(&bar->v_full[st]), (uint32_t)(gi >> 1) & 1, ctl) &&
+                 mbar_wait(smem_u32(&bar->p_full[w]), (uint32_t)gp[w] & 1, ctl) &&
+                 (freed || mbar_wait(smem_u32(&bar->o_free), (uint32_t)(n - 1) & 1, ctl));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            freed = true;
+            ++gp[w];
+            tc_fence_after();
+            const uint32_t vlo = (uint32_t)sw128_desc(s_v + st * G::TILE, ATOM, 1024);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < BKV / 16; ++k)
-                umma_f16_ts(tmem + O_COL + w * D, tmem + w * BKV + 8 * k, sw128_desc(vbase + k * 2048, ATOM, 1024),
-                            IDESC_PV, (i > 1 || k > 0) ? 1u : 0u);
-              if (!sg.two || w == 1) umma_commit(smem_u32(&bar->v_empty[st]));
-              if (sg.two ? i == steps : tp + 2 >= sg.n) umma_commit(smem_u32(&bar->o_full[w]));
+                umma_f16_ts(tmem + O_COL + w * D, tmem + w * BKV + 8 * k, desc_of(vlo + k * (2048 >> 4)), IDESC_PV,
+                            (i > 1 || k > 0) ? 1u : 0u);
+              if (!two || w == 1) umma_commit(smem_u32(&bar->v_empty[st]));
+              if (two ? i == steps : tp + 2 >= sn) umma_commit(smem_u32(&bar->o_full[w]));
             }
-            const int ts = sg.two ? i : 2 * i + w;  // tile of S_w(i)
-            if (i < steps && ts < sg.n) {
-              const int gi = gt + ts, st = gi & 1;
-              if (!mbar_wait(smem_u32(&bar->k_full[st]), (uint32_t)(gi >> 1) & 1, ctl)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t qbase = s_q + (sg.two ? w * G::TILE : 0), kbase = s_k + st * G::TILE;
+            __syncwarp();
+          }
+          const int ts = two ? i : 2 * i + w;  // tile of S_w(i)
+          if (ok && i < steps && ts < sn) {
+            const int gi = gt + ts, st = gi & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar->k_full[st]), (uint32_t)(gi >> 1) & 1, ctl));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t qlo = (uint32_t)sw128_kmajor_desc(s_q + (two ? w * G::TILE : 0));
+            const uint32_t klo = (uint32_t)sw128_kmajor_desc(s_k + st * G::TILE);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * ATOM + (k & 3) * 32;
-                umma_f16(tmem + w * BKV, sw128_kmajor_desc(qbase + off), sw128_kmajor_desc(kbase + off), IDESC_S,
-                         k > 0 ? 1u : 0u);
+                const uint32_t off = ((k >> 2) * ATOM + (k & 3) * 32) >> 4;
+                umma_f16(tmem + w * BKV, desc_of(qlo + off), desc_of(klo + off), IDESC_S, k > 0 ? 1u : 0u);
               }
               umma_commit(smem_u32(&bar->s_full[w]));
-              if (!sg.two || w == 1) umma_commit(smem_u32(&bar->k_empty[st]));
-              if (ts == sg.n - 1 && (!sg.two || w == 1)) umma_commit(smem_u32(&bar->q_empty));
+              if (!two || w == 1) umma_commit(smem_u32(&bar->k_empty[st]));
+              if (ts == sn - 1 && (!two || w == 1)) umma_commit(smem_u32(&bar->q_empty));
             }
+            __syncwarp();
           }
         }
-        gt += sg.n;
-        x += sg.n;
       }
-      umma_commit(smem_u32(&bar->drain));
-      int zero = 0;
-      const WaitCtl dctl{&zero, nullptr, p.limit_ns};
-      mbar_wait(smem_u32(&bar->drain), 0, dctl);
+      gt += sn;
+      x += sn;
     }
+    if (elect_one()) umma_commit(smem_u32(&bar->drain));
+    __syncwarp();
+    int zero = 0;
+    const WaitCtl dctl{&zero, nullptr, p.limit_ns};
+    mbar_wait(smem_u32(&bar->drain), 0, dctl);
   } else {
     // ---------------- softmax streams
     const int w = (int)(warp - 2) / 4;  // this warp's stream
@@ -350,9 +425,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int W = (p.N + 31) / 32;
     int gt = 0, n = 0, gs = 0, go[2] = {0, 0};
     bool ok = true;
-    for (int64_t x = x_begin; x < x_end && ok; ++n) {
-      const Seg sg = seg_at(p, pre, x, x_end);
-      const Row rw = row_of(p, sg.b);
+    for (int x = x_begin; x < x_end && ok; ++n) {
+      const Seg sg = seg_at(p, pl.pre, x, x_end);
+      const Row rw = row_of(p, pl.len[sg.b]);
       const int my_tile = 2 * sg.pair + (sg.two ? w : 0);
       const int node = my_tile * p.npt + r / p.G;
       const bool live_row = r < p.G * p.npt && node < p.N;
@@ -423,38 +498,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         if (live_warp) {
-          // The scores are read twice (maximum, then weights) rather than held: 128
-          // of them in registers spill.  P of 64 keys takes 32 columns, all read by then.
+          // A tile with hidden keys gets -inf over their scores in tensor memory first,
+          // so the common path below carries no masks.
           int first_key = 0;  // committed tile: first visible column
-          bool masked = draft;
           if (!draft) {
             const int start = min(rw.lo + t * BKV, rw.len - BKV);
             first_key = max(rw.lo + t * BKV, tmin) - start;
-            masked = __any_sync(0xffffffffu, first_key > 0);
           }
-          auto mask_half = [&](int h, uint32_t (&rr)[2][32]) {
-            if (draft) {
+          if (__any_sync(0xffffffffu, draft || first_key > 0)) {
+#pragma unroll 1
+            for (int c = 0; c < BKV / 32; ++c) {
+              const int fk = first_key - c * 32;
+              const uint32_t vis = draft ? (c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3])
+                                         : (fk <= 0 ? 0xffffffffu : fk >= 32 ? 0u : 0xffffffffu << fk);
+              uint32_t rr[32];
+              tmem_ld_32x32b_x32(scol + c * 32, rr);
+              tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (!((see[2 * h + (e >> 5)] >> (e & 31)) & 1u)) rr[e >> 5][e & 31] = 0xff800000u;  // -inf
-            } else {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (h * 64 + e < first_key) rr[e >> 5][e & 31] = 0xff800000u;
+              for (int e = 0; e < 32; ++e)
+                if (!((vis >> e) & 1u)) rr[e] = 0xff800000u;  // -inf
+              tmem_st_32x32b_x32(scol + c * 32, rr);
             }
-          };
+            tmem_wait_st();
+          }
+          // The scores are read twice (maximum, then weights), 32 at a time with the
+          // next 32 on their way: 128 of them in registers spill.
+          uint32_t sr[2][32];
           float mx8[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+          tmem_ld_32x32b_x32(scol, sr[0]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t rr[2][32];
-            tmem_ld_32x32b_x32(scol + h * 64, rr[0]);
-            tmem_ld_32x32b_x32(scol + h * 64 + 32, rr[1]);
+          for (int c = 0; c < 4; ++c) {
             tmem_wait_ld();
-            if (masked) mask_half(h, rr);
+            tmem_ld_32x32b_x32(scol + ((c + 1) & 3) * 32, sr[(c + 1) & 1]);  // the last: the weights' first
 #pragma unroll
-            for (int e = 0; e < 64; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(rr[e >> 5][e & 31]));
+            for (int e = 0; e < 32; e += 2)
+              mx8[(e >> 1) & 7] = fmaxf(fmaxf(mx8[(e >> 1) & 7], __uint_as_float(sr[c & 1][e])),
+                                        __uint_as_float(sr[c & 1][e + 1]));
           }
           const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                  fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
@@ -483,28 +564,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           const float ms = m_used == -INFINITY ? 0.0f : m_used * p.scale_log2;
-          float ls8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          // weights two at a time (packed fp32 multiply-adds and sums)
+          const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), ms2 = pack_f32x2(-ms, -ms);
+          uint64_t ls4[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of zeros
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t rr[2][32], pk[32];
-            tmem_ld_32x32b_x32(scol + h * 64, rr[0]);
-            tmem_ld_32x32b_x32(scol + h * 64 + 32, rr[1]);
+          for (int c = 0; c < 4; ++c) {  // P of 32 keys takes 16 columns, all read by then
+            uint32_t pk[16];
             tmem_wait_ld();
-            if (masked) mask_half(h, rr);
+            if (c < 3) tmem_ld_32x32b_x32(scol + (c + 1) * 32, sr[(c + 1) & 1]);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              float q[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                q[e] = ex2f(fmaf(__uint_as_float(rr[c >> 2][(c & 3) * 8 + e]), p.scale_log2, -ms));
-                ls8[e] += q[e];
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) pk[4 * c + e] = Half<F16>::pack2(q[2 * e], q[2 * e + 1]);
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              unpack_f32x2(fma_f32x2(pack_u32x2(sr[c & 1][2 * e], sr[c & 1][2 * e + 1]), sc2, ms2), a, b);
+              a = ex2f(a);
+              b = ex2f(b);
+              ls4[e & 3] = add_f32x2(ls4[e & 3], pack_f32x2(a, b));
+              pk[e] = Half<F16>::pack2(a, b);
             }
-            tmem_st_32x32b_x32(scol + h * 32, pk);
+            tmem_st_32x32b_x16(scol + c * 16, pk);
           }
-          l += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
+          {
+            float a, b;
+            unpack_f32x2(add_f32x2(add_f32x2(ls4[0], ls4[1]), add_f32x2(ls4[2], ls4[3])), a, b);
+            l += a + b;
+          }
           tmem_wait_st();
         }
         first = false;
@@ -545,11 +628,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // one row tile: each stream takes half of the columns of both O
       const int c_lo = sg.two ? 0 : w * (D / 64), c_hi = sg.two ? D / 32 : (w + 1) * (D / 64);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const int64_t prow = ((int64_t)blockIdx.x * 2 + (x == x_begin ? 0 : 1)) * 256 + (sg.two ? w * 128 : 0) + r;
+      // pieces: a warp's 32 rows are neighbours for each column, so its stores are whole lines
+      float* part = p.part + ((((int64_t)blockIdx.x * 2 + (x == x_begin ? 0 : 1)) * 2 + (sg.two ? w : 0)) * (D + 2)) * 128 + r;
       if (!whole && c_lo == 0) {
-        float* ml = p.part + (int64_t)gridDim.x * 512 * D + prow * 2;
-        ml[0] = depth >= 0 ? m_used : -INFINITY;
-        ml[1] = depth >= 0 ? l : 0.0f;
+        part[D * 128] = depth >= 0 ? m_used : -INFINITY;
+        part[(D + 1) * 128] = depth >= 0 ? l : 0.0f;
       }
 #pragma unroll 1
       for (int c = c_lo; c < c_hi; ++c) {
@@ -581,10 +664,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             pk.w = depth >= 0 ? Half<F16>::pack2(v[8 * q + 6] * k, v[8 * q + 7] * k) : 0u;
             dst[q] = pk;
           }
-        } else if (depth >= 0) {
-          float4* dst = reinterpret_cast<float4*>(p.part + prow * D + c * 32);
+        } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int e = 0; e < 32; ++e) part[(c * 32 + e) * 128] = v[e];
         }
       }
       tc_fence_before();
@@ -595,6 +677,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's plan may be made now
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -602,56 +685,70 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // Joins the pieces of each cut unit.  CTA column c does so for the unit whose
-// second piece is CTA c's first; blockIdx.y deals its rows.  One warp a row.
+// second piece is CTA c's first; blockIdx.y deals its rows and columns: a warp
+// takes 32 rows (a row a lane, as the pieces are stored) and 16 columns.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) tree_tc_merge_kernel(const Params p, int ctas) {
-  extern __shared__ int64_t pre[];
-  fill_prefix(p, pre);
+  extern __shared__ int mem[];
+  const Plan pl = make_plan(p, mem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
-  const int64_t total = pre[p.B];
-  const int64_t x = cta_begin(total, c, ctas);
-  if (x >= cta_begin(total, c + 1, ctas)) return;
-  const Seg sg = seg_at(p, pre, x, total);
-  if (sg.t0 == 0) return;  // a unit starts here
-  // first CTA of the unit: c is its second iff the CTA before c (with work) holds the unit's start
-  int c0 = c - 1;
-  while (c0 > 0 && cta_begin(total, c0, ctas) == x) --c0;  // CTAs without work
-  if (cta_begin(total, c0, ctas) > sg.u0) return;
-  const int64_t u_end = sg.u0 + sg.units_t;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int W = (p.N + 31) / 32;
-  constexpr int PER = D / 32;
-  const int rows = sg.two ? 256 : 128;
-  for (int rr = blockIdx.y * 8 + warp; rr < rows; rr += gridDim.y * 8) {
-    const int r = rr & 127;
-    const int node = (2 * sg.pair + (rr >> 7)) * p.npt + r / p.G;
-    if (r >= p.G * p.npt || node >= p.N) continue;
-    const bool used = (p.mask[((int64_t)sg.b * p.N + node) * W + (node >> 5)] >> (node & 31)) & 1u;
-    float acc[PER], m = -INFINITY, l = 0.0f;
+  const int total = pl.pre[p.B];
+  const Deal deal(total, ctas);
+  const int x = deal.begin(c);
+  if (x >= deal.begin(c + 1)) return;
+  const Seg sg = seg_at(p, pl.pre, x, total);
+  // Every CTA has a tile or more once c has one (the first ones get the extra
+  // tiles), so the piece before this one is CTA c - 1's.
+  if (sg.t0 == 0 || deal.begin(c - 1) > sg.u0) return;
+  const int u_end = sg.u0 + sg.units_t;
+  const int lane = threadIdx.x & 31;
+  int k_end = c + 1;  // past the last piece's CTA
+  while (k_end < ctas && deal.begin(k_end) < u_end && deal.begin(k_end + 1) > deal.begin(k_end)) ++k_end;
+  constexpr int CG = D / 16;  // column groups
+  const int jobs = (sg.two ? 8 : 4) * CG;
+  for (int job = blockIdx.y * 8 + (threadIdx.x >> 5); job < jobs; job += gridDim.y * 8) {
+    const int rg = job / CG, cg = job - rg * CG;
+    const int r = (rg & 3) * 32 + lane;
+    const int node = (2 * sg.pair + (rg >> 2)) * p.npt + r / p.G;
+    const bool in = r < p.G * p.npt && node < p.N;
+    // piece k of the unit: CTA k's first piece unless the unit starts inside CTA k's work
+    auto piece = [&](int k) {
+      return p.part + ((((int64_t)k * 2 + (deal.begin(k) >= sg.u0 ? 0 : 1)) * 2 + (rg >> 2)) * (D + 2)) * 128 + r;
+    };
+    float acc[16], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.0f;
-    const float* ml = p.part + (int64_t)ctas * 512 * D;
-    for (int k = c0; used && k < ctas; ++k) {
-      const int64_t kb = cta_begin(total, k, ctas);
-      if (kb >= u_end) break;
-      if (cta_begin(total, k + 1, ctas) == kb) continue;
-      const int64_t prow = ((int64_t)k * 2 + (kb >= sg.u0 ? 0 : 1)) * 256 + rr;
-      const float mk = ml[prow * 2], lk = ml[prow * 2 + 1];
-      if (mk == -INFINITY) continue;
+    for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+    for (int k = c - 1; k < k_end; ++k) {
+      const float* src = piece(k);
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = src[(cg * 16 + e) * 128];
+      const float mk = src[D * 128], lk = src[(D + 1) * 128];
       const float mn = fmaxf(m, mk);
+      // rows of a piece that saw nothing (and rows that are no node's) hold anything
+      const bool got = in && mk != -INFINITY;
       const float a = m == -INFINITY ? 0.0f : ex2f((m - mn) * p.scale_log2), b = ex2f((mk - mn) * p.scale_log2);
-      const float* src = p.part + prow * D + lane * PER;
+      if (got) {
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = acc[e] * a + src[e] * b;
-      l = l * a + lk * b;
-      m = mn;
+        for (int e = 0; e < 16; ++e) acc[e] = fmaf(acc[e], a, v[e] * b);
+        l = fmaf(l, a, lk * b);
+        m = mn;
+      }
     }
+    if (!in) continue;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(
-        p.out + (((int64_t)sg.b * p.N + node) * p.H + sg.g * p.G + r % p.G) * D + lane * PER);
+    uint4* dst = reinterpret_cast<uint4*>(
+        p.out + (((int64_t)sg.b * p.N + node) * p.H + sg.g * p.G + r % p.G) * D + cg * 16);
 #pragma unroll
-    for (int e = 0; e < PER / 2; ++e) dst[e] = Half<F16>::pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    for (int q = 0; q < 2; ++q) {
+      uint4 pk;
+      pk.x = Half<F16>::pack2(acc[8 * q] * inv, acc[8 * q + 1] * inv);
+      pk.y = Half<F16>::pack2(acc[8 * q + 2] * inv, acc[8 * q + 3] * inv);
+      pk.z = Half<F16>::pack2(acc[8 * q + 4] * inv, acc[8 * q + 5] * inv);
+      pk.w = Half<F16>::pack2(acc[8 * q + 6] * inv, acc[8 * q + 7] * inv);
+      dst[q] = pk;
+    }
   }
 }
 
@@ -659,15 +756,21 @@ template <int D, bool F16>
 nc_status launch_t(const CUtensorMap& mq, const CUtensorMap& mc, const CUtensorMap& md, const Params& p, int ctas,
                    cudaStream_t stream) {
   using G = Geo<D>;
-  if (cudaFuncSetAttribute(tree_tc_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM_BYTES) !=
-      cudaSuccess)
-    return NC_ERR_CUDA;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_done[dev]) {
+    if (cudaFuncSetAttribute(tree_tc_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM_BYTES) !=
+        cudaSuccess)
+      return NC_ERR_CUDA;
+    if (dev < 64) attr_done[dev] = true;
+  }
   tree_tc_kernel<D, F16><<<ctas, NUM_THREADS, G::SMEM_BYTES, stream>>>(mq, mc, md, p);
   if (cudaGetLastError() != cudaSuccess) return NC_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas, 8);
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = (size_t)(p.B + 1) * 8;
+  cfg.dynamicSmemBytes = (size_t)(2 * p.B + 1) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its prologue overlaps the products
@@ -679,8 +782,12 @@ nc_status launch_t(const CUtensorMap& mq, const CUtensorMap& mc, const CUtensorM
 
 }  // namespace tree_tc
 
+// At most 2^15 units of at most 2^22 / 128 + 1 tiles: linear tile indices fit 32 bits.
 bool tree_attention_tc_fits(int B, int N, int H, int Hkv, int window) {
-  return B <= tree_tc::kMaxB && H / Hkv <= tree_tc::BM && (window <= 0 || window > tree_tc::BKV);
+  const int G = H / Hkv;
+  if (G > tree_tc::BM) return false;
+  const int tiles_r = (N + tree_tc::BM / G - 1) / (tree_tc::BM / G);
+  return B <= tree_tc::kMaxB && (int64_t)B * Hkv * ((tiles_r + 1) / 2) <= (1 << 15) && (window <= 0 || window > tree_tc::BKV);
 }
 
 size_t tree_attention_tc_bytes(int D) { return (size_t)device_sm_count() * 512 * (D + 2) * 4; }

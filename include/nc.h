@@ -633,7 +633,7 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * (q_row_stride >= H D, a multiple of 8); kv [B, N, 2, Hkv, D]; cache
  * [B, T_max, 2, Hkv, D]; out [B, N, H, D]; 16-bit in format dtype.  lens [B] is
  * clamped to [0, T_max]; positions at and past it are not read.  D in {64,
- * 128}, 1 <= N <= 128, B <= 65535, H <= 4096.  K and V of committed positions
+ * 128}, 1 <= N <= 128, 1 <= T_max <= 2^22, B <= 65535, H <= 4096.  K and V of committed positions
  * inside the root's window and of used nodes must be finite.  workspace: at
  * least nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where
  * that is 0); calls that overlap in time need one each.  The result is the same

@@ -9,22 +9,28 @@
 //   token = the first kept index, in index order, whose running mass exceeds
 //   u times the kept mass; logprob = log(w_token / kept mass)
 //
-// A token's index changes when a running sum is misplaced by one border, so the
-// weights are computed in fp64 and summed as 64-bit integers in units of 2^-sh
-// (sh = 62 less the bits of V, 51 at most: V weights of 1 do not overflow): integer sums do not
-// depend on their order, so neither the split of a row over threads nor a race
-// changes a result.  A weight below half a unit counts as 0.
+// A token's index changes when a running sum is misplaced by one border.  The
+// definition here is in integers: a weight is computed in fp64 and rounded to
+// units of 2^-sh (sh = 62 less the bits of V, 51 at most: V weights of 1 do not
+// overflow), and sums are exact whatever their order.  A row is first tried
+// with fp32 weights, whose sums carry a bound of their error: where no border
+// (of top-p's share, of min-p, of the token's own interval) lies within it, the
+// integers would give the same token; only else are they computed.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "nc_internal.h"
 
 namespace nc {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+// Filters: a histogram of the logits (kBins equal bins from the maximum down)
+// finds the bin where top-k cuts and a bracket of bins where top-p does; the
+// tokens of those bins, at most one a thread, are sorted and cut exactly.
+constexpr int kBins = 2048;
 
 struct SampleParams {
   const float* logits;  // [M][ld]
@@ -37,6 +43,7 @@ struct SampleParams {
   int32_t* tokens;           // [M]
   float* logprob;            // [M] or null
   int V, sh;
+  int half;  // the histogram keeps a bin's mass as two sums of this many bits a token
 };
 
 // Order-preserving map of a logit to 32 bits; -0 equals +0, NaN is below
@@ -51,223 +58,924 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key >> 31) ? (key & 0x7fffffffu) : ~key);
 }
 
-// exp((l - mx) / T) in units of 2^-sh, rounded to the nearest: 2^y with
-// y = (l - mx) log2(e) / T split into the nearest integer and a remainder in
-// [-1/2, 1/2], whose exponential is the Taylor series of e^(f ln 2) to the
-// 11th power (remainder 7e-15).  c = log2(e) / T.  The row's maximum counts 1
-// whatever it is (also +inf), -inf and NaN count 0.
-__device__ __forceinline__ int64_t weight_of(float l, float mx, double c, int sh) {
-  if (l == mx) return (int64_t)1 << sh;
-  const double d = (double)l - (double)mx;
-  const double y = d * c;
-  if (!(y > -(double)(sh + 2))) return 0;  // NaN, -inf and what rounds to 0
-  constexpr double kMagic = 6755399441055744.0;  // 1.5 2^52: adding it rounds to an integer
-  const double t = y + kMagic;
-  const int n = (int)__double2loint(t);
-  const double f = y - (t - kMagic);
-  // ln(2)^k / k!
-  double r = 4.4455382718708116e-10 * f + 7.0549116208011233e-09;
-  r = fma(r, f, 1.0178086009239699e-07);
-  r = fma(r, f, 1.3215486790144309e-06);
-  r = fma(r, f, 1.5252733804059840e-05);
-  r = fma(r, f, 1.5403530393381609e-04);
-  r = fma(r, f, 1.3333558146428443e-03);
-  r = fma(r, f, 9.6181291076284772e-03);
-  r = fma(r, f, 5.5504108664821580e-02);
-  r = fma(r, f, 2.4022650695910071e-01);
-  r = fma(r, f, 6.9314718055994531e-01);
-  r = fma(r, f, 1.0);
-  const double s = __hiloint2double(__double2hiint(r) + ((n + sh) << 20), __double2loint(r));  // r 2^(n + sh)
-  return __double2ll_rn(s);
+// 2^(j / 32)
+__constant__ double kExp2[32] = {
+    1, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.6457554781539649,
+    1.681792830507429, 1.7186192981224779, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002};
+
+// A row's exponential: exp((l - mx) / T) in units of 2^-sh, rounded to nearest.
+// 2^y, y = (l - mx) log2(e) / T, in fp64: y = (32 n + j) / 32 + f with |f| <=
+// 1/64, 2^f by the Taylor series of e^(f ln 2) to the 5th power (remainder
+// 2.2e-15) times 2^(j/32).  The maximum counts 1 whatever it is (also +inf);
+// -inf and NaN count 0.
+struct Expo {
+  float mx, c32, least;  // c32: log2(e) / T; y below `least` rounds to 0
+  double mxd, c;
+  int shx;               // sh << 20
+  const double* tab;     // kExp2 in shared memory
+
+  __device__ Expo(float mx_, float T, int sh, const double* tab_)
+      : mx(mx_), c32((float)(1.4426950408889634 / (double)T)), least(-(float)(sh + 1)),
+        mxd(mx_ == INFINITY ? 0.0 : (double)mx_), c(1.4426950408889634 / (double)T), shx(sh << 20), tab(tab_) {}
+
+  static constexpr int64_t kRaw0 = 0x4330000000000000ll;  // the bits of 2^52: what 0 looks like
+
+  // The weight as the low bits of 2^52 + weight: sums of these are exact too.
+  __device__ __forceinline__ int64_t raw(float l) const {
+    const bool counts = l == mx || (l - mx) * c32 > least;
+    const double d = l == mx ? 0.0 : (double)l - mxd;
+    constexpr double kMagic = 6755399441055744.0 / 32;  // 1.5 2^52 / 32: adding it rounds to 1/32
+    const double t = fma(d, c, kMagic);
+    const int nj = __double2loint(t);
+    const double f = fma(d, c, kMagic - t);
+    // ln(2)^k / k!
+    double r = 1.3333558146428443e-03;
+    r = fma(r, f, 9.618129107628477e-03);
+    r = fma(r, f, 5.550410866482158e-02);
+    r = fma(r, f, 2.402265069591007e-01);
+    r = fma(r, f, 6.931471805599453e-01);
+    r = fma(r, f, 1.0);
+    r *= tab[nj & 31];
+    // r 2^(n + sh) <= 2^51, rounded to an integer by adding 2^52
+    const int hi = __double2hiint(r) + ((nj & ~31) << 15) + shx;
+    return __double_as_longlong(__hiloint2double(counts ? hi : 0, __double2loint(r)) + 4503599627370496.0);
+  }
+  __device__ __forceinline__ int64_t operator()(float l) const { return raw(l) - kRaw0; }
+};
+
+// The same as an fp32 number (1 for the maximum): y = n + f in two fp32 parts (the
+// difference's and the product's low parts kept), 2^f by the hardware, n into the
+// exponent.
+struct Expo32 {
+  float mx, least, c_hi, c_lo;
+  // Relative error of a weight: 2^-22 (2^f), 2^-25 ln 2 (f), and, where |l| > |mx|
+  // makes the difference's low part inexact, 2^-24 |y| ln 2; sums of four add
+  // three times 2^-24.
+  static constexpr double kErr = 5e-7, kErrY = 4.5e-8;
+
+  __device__ Expo32(float mx_, float T) : mx(mx_) {
+    const double c = 1.4426950408889634 / (double)T;
+    c_hi = (float)c;
+    c_lo = (float)(c - (double)c_hi);
+    least = mx_ - (float)(100.0 / c);  // below it a weight is 2^-100: nothing beside 1
+  }
+  __device__ static bool usable(float mx, float T) {
+    return T > 1e-20f && T < 1e20f && fabsf(mx) < 1e5f * T;
+  }
+  __device__ __forceinline__ float operator()(float l, float& y) const {
+    const float lc = fmaxf(l, least);  // also -inf and NaN
+    const float d = lc - mx, d_lo = lc - (d + mx);
+    y = d * c_hi;
+    const float y_lo = fmaf(d_lo, c_hi, fmaf(d, c_lo, fmaf(d, c_hi, -y)));
+    const float t = y + 12582912.0f;  // 1.5 2^23: the nearest integer in the low bits
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((y - (t - 12582912.0f)) + y_lo));
+    return __int_as_float(__float_as_int(w) + (__float_as_int(t) << 23));
+  }
+};
+
+// One row as its CTA walks it: from a 16-byte boundary at or before its start
+// (position off is token 0), in a contiguous segment per warp, which passes that
+// depend on the index order rely on.
+struct Row {
+  const float* base;
+  int off, end;    // tokens are the positions [off, end)
+  int seg0, seg1;  // this warp's
+  int per;         // positions a segment, a multiple of 128
+};
+
+__device__ __forceinline__ float4 load4(const Row& r, int j) {
+  if (j >= r.off && j + 4 <= r.end) return *reinterpret_cast<const float4*>(r.base + j);
+  float4 v = make_float4(NAN, NAN, NAN, NAN);
+  if (j >= r.off && j < r.end) v.x = r.base[j];
+  if (j + 1 >= r.off && j + 1 < r.end) v.y = r.base[j + 1];
+  if (j + 2 >= r.off && j + 2 < r.end) v.z = r.base[j + 2];
+  if (j + 3 >= r.off && j + 3 < r.end) v.w = r.base[j + 3];
+  return v;
 }
 
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, T* red, F f) {
+// f(position, four logits) for the warp's positions, each lane four neighbours
+// at a time; positions outside the row come as NaN.  U loads are in flight.
+template <int U, typename F>
+__device__ __forceinline__ void walk4(const Row& r, F f) {
+#pragma unroll 1
+  for (int j0 = r.seg0 + (threadIdx.x & 31) * 4; j0 < r.seg1; j0 += 128 * U) {
+    float4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (j0 + k * 128 < r.seg1) v[k] = load4(r, j0 + k * 128);
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (j0 + k * 128 < r.seg1) f(j0 + k * 128, v[k]);
+  }
+}
+
+template <int U, typename F>
+__device__ __forceinline__ void walk(const Row& r, F f) {
+  walk4<U>(r, [&](int j, const float4& v) {
+    f(j, v.x);
+    f(j + 1, v.y);
+    f(j + 2, v.z);
+    f(j + 3, v.w);
+  });
+}
+
+// Order of the tokens: larger first (logit, then lower index).
+__device__ __forceinline__ uint64_t code_of(float l, int pos) {
+  return ((uint64_t)key_of(l) << 32) | (uint32_t)~pos;
+}
+
+constexpr int kTopBins = 256;  // histogram of the threads' maxima
+constexpr int kListMax = 256;  // nuclei of more tokens than this are not listed whole
+
+template <int NT>
+struct Smem {
+  double tab[32];
+  int64_t red[32];
+  float redf[3][32];
+  int64_t seg[32];
+  union {
+    struct {
+      uint32_t cnt[kBins], lo[kBins], hi[kBins];  // tokens; mass in 2^-(2 half), as hi 2^half + lo
+    } h;
+    struct {
+      uint64_t buf[2 * NT];
+      int64_t mass[NT];
+      float logit[NT];
+    } s;
+  };
+  uint64_t cand[NT];
+  int ncand, bk, cnt_bk, b1, b2, cnt_b1, cnt_b2, pick;
+};
+
+struct Add {
+  template <typename T>
+  __device__ T operator()(T a, T b) const {
+    return a + b;
+  }
+};
+struct Min {
+  __device__ int operator()(int a, int b) const { return min(a, b); }
+};
+
+template <int NT, typename T, typename F>
+__device__ __forceinline__ T block_reduce(T v, int64_t* red, F f, T none) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<T*>(red)[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = red[threadIdx.x & 31];
+  const int lane = threadIdx.x & 31;
+  v = lane < NT / 32 ? reinterpret_cast<T*>(red)[lane] : none;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
-struct Add {
-  __device__ int64_t operator()(int64_t a, int64_t b) const { return a + b; }
-};
-struct MaxU64 {
-  __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+// Inclusive sums of one 64-bit value a thread over the first `threads` threads.
+template <int NT, typename T>
+__device__ __forceinline__ T block_scan(T v, int64_t* red, int threads = NT) {
+  static_assert(sizeof(T) == 8, "red holds 64-bit values");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T* rd = reinterpret_cast<T*>(red);
+  if (threadIdx.x < threads) v = warp_scan(v);
+  __syncthreads();
+  if (lane == 31) rd[warp] = threadIdx.x < threads ? v : T(0);
+  __syncthreads();
+  if (warp == 0 || threadIdx.x >= threads) return v;
+  const T w = warp_scan(lane < warp ? rd[lane] : T(0));
+  return v + __shfl_sync(0xffffffffu, w, 31);
+}
+
+struct Filter {
+  int k;    // 0: off
+  float p;  // >= 1: off
 };
 
-// One CTA a row; every warp owns a contiguous segment of the row for the steps
-// that depend on the index order.
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
-  __shared__ int64_t red[kWarps];
-  __shared__ int64_t seg[kWarps];
+// The code of the last token that top-k and top-p keep, for any row: bisection
+// over the keys, a pass of the row each.  For rows whose cut falls among more
+// more tokens of one bin than the block has threads (heavy ties, logits spread over hundreds).
+template <int NT>
+__device__ __noinline__ uint64_t cut_by_bisection(const Row& r, const Filter& f, const Expo& weight, Smem<NT>& sm) {
+  const uint32_t kmax = key_of(weight.mx);
+  uint32_t cut = 0;
+  int64_t ties = INT_MAX;
+  auto count_from = [&](uint32_t key) {  // tokens at or above it
+    int64_t n = 0;
+    walk<2>(r, [&](int, float l) { n += key_of(l) >= key; });
+    return block_reduce<NT>(n, sm.red, Add{}, (int64_t)0);
+  };
+  auto mass_above = [&](uint32_t key) {
+    int64_t z = 0;
+    walk<2>(r, [&](int, float l) {
+      if (key_of(l) > key) z += weight(l);
+    });
+    return block_reduce<NT>(z, sm.red, Add{}, (int64_t)0);
+  };
+  if (f.k > 0) {
+    uint32_t lo = 1, hi = kmax;  // the largest key with at least k tokens from it on
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2 + 1;
+      if (count_from(mid) >= f.k)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    cut = lo;
+    ties = f.k - count_from(cut + 1);
+  }
+  if (!(f.p >= 1.0f)) {
+    int64_t z = mass_above(cut);
+    if (cut > 0) {
+      const int64_t nt = count_from(cut) - count_from(cut + 1);
+      z += (nt < ties ? nt : ties) * weight(value_of(cut));
+    }
+    const double want = (f.p > 0.0f ? (double)f.p : 0.0) * (double)z;
+    uint32_t lo = cut, hi = kmax;  // the smallest key with less than `want` above it
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      if ((double)mass_above(mid) < want)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    const int64_t w = weight(value_of(lo));
+    int64_t n = INT_MAX;  // of its ties, those with less than `want` before them
+    if (w > 0) {
+      const double q = ceil((want - (double)mass_above(lo)) / (double)w);
+      n = q < 1.0 ? 1 : (q > (double)INT_MAX ? INT_MAX : (int64_t)q);
+    }
+    ties = lo == cut ? (ties < n ? ties : n) : n;
+    cut = lo;
+  }
+  // the index of the last kept tie
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n = 0;
+  walk<2>(r, [&](int, float l) { n += l == l && key_of(l) == cut; });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  __syncthreads();
+  if (lane == 0) sm.seg[warp] = n;
+  if (threadIdx.x == 0) sm.pick = -1;
+  __syncthreads();
+  int64_t before = 0;
+  for (int w = 0; w < warp; ++w) before += sm.seg[w];
+  if (before < ties && ties <= before + n) {
+    int64_t seen = before;
+    for (int j = r.seg0; j < r.seg1 && seen < ties; j += 32) {
+      const int i = j + lane;
+      const bool tie = i >= r.off && i < r.end && i < r.seg1 && r.base[i] == r.base[i] && key_of(r.base[i]) == cut;
+      uint32_t bal = __ballot_sync(0xffffffffu, tie);
+      const int here = __popc(bal);
+      if (seen + here >= ties) {
+        for (int64_t q = seen + 1; q < ties; ++q) bal &= bal - 1;
+        if (lane == 0) sm.pick = j + __ffs(bal) - 1;
+      }
+      seen += here;
+    }
+  }
+  __syncthreads();
+  const int at = sm.pick;
+  return at >= 0 ? ((uint64_t)cut << 32) | (uint32_t)~at : (uint64_t)cut << 32;
+}
+
+// Bitonic sort of one value a thread, largest first, over the first P threads
+// (a power of two; the others only keep step); buf: 2 NT values.
+template <int NT>
+__device__ __forceinline__ uint64_t block_sort(uint64_t v, int P, uint64_t* buf) {
+  const int tid = threadIdx.x;
+  const bool in = (tid & ~31) < P;  // the warp takes part
+  int flip = 0;
+#pragma unroll 1
+  for (int k = 2; k <= P; k <<= 1)
+#pragma unroll 1
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      uint64_t o = 0;
+      if (j >= 32) {
+        uint64_t* b = buf + flip * NT;
+        flip ^= 1;
+        if (in) b[tid] = v;
+        __syncthreads();
+        if (in) o = b[tid ^ j];
+      } else if (in) {
+        o = __shfl_xor_sync(0xffffffffu, v, j);
+      }
+      const bool big = ((tid & j) == 0) == ((tid & k) == 0);
+      v = (v > o) == big ? v : o;
+    }
+  return v;
+}
+
+__device__ __forceinline__ int pow2_from(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+// The last steps where the n <= NT candidates (sm.cand) are known to hold every
+// kept token: sorted by likelihood, cut, sorted by index, and the running mass
+// tells the token.  k: how many top-k leaves.  Without top-k the mass that top-p
+// is a share of is known to lie in [z_lo, z_hi]; false if that does not settle
+// the cut.  Called by the whole block.
+template <int NT>
+__device__ __noinline__ bool pick_from_list(int n, int k, float tp, int64_t z_lo, int64_t z_hi, int64_t wmin, float u,
+                                            const Expo& weight, float T, Smem<NT>& sm, const SampleParams& p, int row,
+                                            int off) {
+  const int tid = threadIdx.x;
+  const bool use_p = !(tp >= 1.0f);
+  const int P = pow2_from(n);
+  const uint64_t code = block_sort<NT>(tid < n ? sm.cand[tid] : 0ull, P, sm.s.buf);
+  const float l = value_of((uint32_t)(code >> 32));
+  int64_t w = tid < n ? weight(l) : 0;
+  int64_t cum = block_scan<NT>(w, sm.red, (P + 31) & ~31);
+  if (k < n) n = k;
+  if (use_p && z_lo < 0) {  // top-k's mass
+    if (tid == n - 1) sm.seg[0] = cum;
+    __syncthreads();
+    z_lo = z_hi = sm.seg[0];
+  }
+  const double pp = tp > 0.0f ? (double)tp : 0.0, b = (double)(cum - w);
+  // top-p and min-p keep a first part of the order as well
+  bool keep = tid < n && w >= wmin;
+  if (use_p) {
+    if (__syncthreads_or(keep && tid > 0 && b >= pp * (double)z_lo && b < pp * (double)z_hi)) return false;
+    keep = keep && (tid == 0 || b < pp * (double)z_lo);
+  }
+  n = __syncthreads_count(keep);
+  if (tid == n - 1) sm.seg[0] = cum;  // the kept mass
+  if (tid < n) {
+    sm.s.mass[tid] = w;
+    sm.s.logit[tid] = l;
+  }
+  // by index: ~position is in the code's low word, so largest first is index order
+  const int Q = pow2_from(n);
+  const uint64_t by_pos = block_sort<NT>(tid < n ? (code << 32) | (uint32_t)tid : 0ull, Q, sm.s.buf);
+  __syncthreads();
+  const int64_t total = sm.seg[0];
+  const int rank = (int)(uint32_t)by_pos;
+  w = tid < n ? sm.s.mass[rank] : 0;
+  cum = block_scan<NT>(w, sm.red, (Q + 31) & ~31);
+  const double target = (u > 0.0f ? (double)u : 0.0) * (double)total;
+  const bool last = target >= (double)total;  // u >= 1: the last kept token
+  if (tid < n && w > 0 && (last ? cum == total : (double)cum > target && (double)(cum - w) <= target)) {
+    p.tokens[row] = (int)~(uint32_t)(by_pos >> 32) - off;
+    if (p.logprob) {
+      const float lt = sm.s.logit[rank];
+      const double z = log((double)total) - (double)p.sh * 0.6931471805599453;
+      p.logprob[row] = (float)((lt == weight.mx ? 0.0 : ((double)lt - (double)weight.mx) / (double)T) - z);
+    }
+  }
+  return true;
+}
+
+// What the histogram found out.
+struct Cut {
+  bool bins, use_k, use_p;
+  float mx, scale;
+  int k, b1, b2, bk;  // top-k's bin; the bracket of top-p's (without it: bk twice)
+  int n1, cnt_above, cnt_bk;  // tokens in the bracket, before it, before bk
+  bool fits;  // the tokens of the bracket and of bk can be sorted
+
+  // Rounded to the nearest bin: never falls where l grows down, which is all that
+  // is asked of it; a float, so comparing needs no conversion.
+  static constexpr float kOne = 8388608.0f;  // 2^23: the sum's last bit is 1
+  __device__ __forceinline__ float fbin(float l) const {
+    const float d = l == mx ? 0.0f : mx - l;
+    return fminf(fmaf(d, scale, kOne), kOne + (float)(kBins - 1));
+  }
+  __device__ __forceinline__ int bin(float l) const { return __float_as_int(fbin(l)) - 0x4b000000; }
+};
+
+// The row's token from its bracket: a pass that sums every segment's sure tokens
+// and lists the bracket's, the cut in the list, then the segment, the warp's
+// share of it and the token.  EXACT: integer weights (and, if the bracket fails,
+// the bisection); else fp32 ones, false where their error leaves it open.
+template <int NT, bool EXACT>
+__device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp, float mp, float u, float T,
+                                           const Expo& we, Smem<NT>& sm, const SampleParams& p, int row) {
+  using A = typename std::conditional<EXACT, int64_t, double>::type;
+  constexpr int NW = NT / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Expo32 wf(q.mx, T);
+  const A wmin = EXACT ? (A)(mp > 0.0f ? __double2ll_ru((double)fminf(mp, 1.0f) * exp2((double)p.sh)) : 0)
+                       : (A)(mp > 0.0f ? fminf(mp, 1.0f) : 0.0f);
+  const bool use_m = mp > 0.0f;
+  // a token's weight; fp32: its share of the error bound, and whether min-p is open
+  float s1 = 0.0f;
+  bool open = false;
+  auto weight = [&](float l) -> A {
+    if constexpr (EXACT) {
+      return we(l);
+    } else {
+      float y;
+      return (A)wf(l, y);
+    }
+  };
+  // small weights are added in fp32 first; beside a large one they would lose their
+  // last bits, which the logprob of a likely token shows
+  auto sum4 = [](float a, float b, float c, float d) -> double {
+    if (fmaxf(fmaxf(a, b), fmaxf(c, d)) > 0.004f) return ((double)a + (double)b) + ((double)c + (double)d);
+    return (double)((a + b) + (c + d));
+  };
+  const float f1 = Cut::kOne + (float)q.b1, f2 = Cut::kOne + (float)q.b2, fk = Cut::kOne + (float)q.bk;
+  if (tid == 0) sm.ncand = 0;
+  __syncthreads();
+  bool good = q.fits;
+  A za = 0, zt = 0, mass = 0;  // before the bracket; all that top-p's share is of; kept of the segment
+  double e1 = 0.0;             // sum of w |y|
+  if (good) {
+    if constexpr (EXACT) {
+      uint64_t sum = 0;  // modulo 2^64 until the 2^52 of every position is taken off
+      if (!q.bins && !use_m) {
+        walk<1>(r, [&](int, float l) { sum += (uint64_t)we.raw(l); });
+        const int lane0 = r.seg0 + lane * 4;
+        sum -= (uint64_t)(lane0 < r.seg1 ? (r.seg1 - lane0 + 127) / 128 * 4 : 0) * (uint64_t)Expo::kRaw0;
+        mass = (A)sum;
+      } else {
+        walk<1>(r, [&](int j, float l) {
+          const int64_t w = we(l);
+          const float b = q.fbin(l);
+          const bool cand = q.bins && l > -INFINITY && b >= f1 && (b <= f2 || (q.use_k && b == fk));
+          const bool sure = !q.bins || b < f1;
+          if (cand) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l, j);
+          za += sure ? w : 0;
+          zt += !cand && (!q.use_k || b < fk) ? w : 0;
+          mass += sure && w >= wmin ? w : 0;
+        });
+      }
+    } else if (!q.bins) {
+      walk4<4>(r, [&](int, const float4& v) {
+        float y0, y1, y2, y3;
+        float w0 = wf(v.x, y0), w1 = wf(v.y, y1), w2 = wf(v.z, y2), w3 = wf(v.w, y3);
+        s1 = fmaf(w0, y0, fmaf(w1, y1, fmaf(w2, y2, fmaf(w3, y3, s1))));
+        if (use_m) {
+          const float m = (float)wmin, near = m * 1e-5f;
+          open = open || fabsf(w0 - m) <= near || fabsf(w1 - m) <= near || fabsf(w2 - m) <= near ||
+                 fabsf(w3 - m) <= near;
+          w0 = w0 >= m ? w0 : 0.0f;
+          w1 = w1 >= m ? w1 : 0.0f;
+          w2 = w2 >= m ? w2 : 0.0f;
+          w3 = w3 >= m ? w3 : 0.0f;
+        }
+        mass += sum4(w0, w1, w2, w3);
+      });
+    } else {
+      walk4<2>(r, [&](int j, const float4& v) {
+        const float l[4] = {v.x, v.y, v.z, v.w};
+        float a[4], t[4], m[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y;
+          const float w = wf(l[e], y), b = q.fbin(l[e]);
+          s1 = fmaf(w, y, s1);
+          const bool cand = l[e] > -INFINITY && b >= f1 && (b <= f2 || (q.use_k && b == fk));
+          const bool sure = b < f1;
+          if (cand) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l[e], j + e);
+          a[e] = sure ? w : 0.0f;
+          t[e] = !cand && (!q.use_k || b < fk) ? w : 0.0f;
+          m[e] = a[e];
+          if (use_m) {
+            open = open || fabsf(w - (float)wmin) <= (float)wmin * 1e-5f;
+            m[e] = w >= (float)wmin ? a[e] : 0.0f;
+          }
+        }
+        const double a4 = sum4(a[0], a[1], a[2], a[3]);
+        za += a4;
+        zt += sum4(t[0], t[1], t[2], t[3]);
+        mass += use_m ? sum4(m[0], m[1], m[2], m[3]) : a4;
+      });
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  }
+  uint64_t cutcode = 0;  // kept: the tokens with at least this code
+  A z_all = 0;
+  if (good && q.bins) {
+    __syncthreads();
+    const int nc = sm.ncand, P = pow2_from(nc);
+    if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = mass;
+    const uint64_t code = block_sort<NT>(tid < nc ? sm.cand[tid] : 0ull, P, sm.s.buf);
+    const A wc = tid < nc ? weight(value_of((uint32_t)(code >> 32))) : A(0);
+    const A cum = block_scan<NT>(wc, sm.red, (P + 31) & ~31);
+    A* cums = reinterpret_cast<A*>(sm.s.mass);
+    cums[tid] = cum;
+    sm.cand[tid] = code;
+    za = block_reduce<NT>(za, sm.red, Add{}, A(0));
+    zt = block_reduce<NT>(zt, sm.red, Add{}, A(0));
+    // how many candidates top-k leaves, then top-p
+    int cut = nc;
+    if (q.use_k) cut = q.bk > q.b2 ? q.n1 + (q.k - q.cnt_bk) : q.k - q.cnt_above;
+    z_all = zt + (nc > 0 ? cums[nc - 1] : A(0));
+    double err = 0.0;
+    if constexpr (!EXACT) {
+      e1 = block_reduce<NT>((double)s1, sm.red, Add{}, 0.0);
+      err = 2.0 * (Expo32::kErr * z_all - Expo32::kErrY * e1);
+    }
+    if (q.use_p) {
+      const double z = (double)(zt + (cut > 0 ? cums[cut - 1] : A(0)));
+      const double want = (tp > 0.0f ? (double)tp : 0.0) * z;
+      int lo = 0, hi = min(q.n1, cut);  // candidates with less than `want` before them
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if ((double)(za + (mid ? cums[mid - 1] : A(0))) < want)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      // the bracket holds the cut
+      good = (q.cnt_above == 0 || (double)za < want) &&
+             (lo < q.n1 || q.b2 == (q.use_k ? q.bk : kBins - 1) ||
+              (q.n1 > 0 && (double)(za + cums[q.n1 - 1]) >= want));
+      if (!EXACT && good) {  // and no token's border is within the error of what is wanted
+        auto before = [&](int i) { return (double)(za + (i ? cums[i - 1] : A(0))); };
+        if (lo == 0)
+          good = q.cnt_above == 0;
+        else
+          good = want - before(lo - 1) > err || (lo == 1 && q.cnt_above == 0);
+        if (lo < min(q.n1, cut) || (lo == q.n1 && q.b2 != (q.use_k ? q.bk : kBins - 1)))
+          good = good && before(lo) - want > err;
+      }
+      cut = q.cnt_above == 0 ? max(lo, 1) : lo;
+    }
+    good = good && cut > 0;
+    if (good) {
+      cutcode = sm.cand[cut - 1];
+      // kept candidates into their segments, in a fixed order
+      A add = 0;
+      for (int i = lane; i < cut; i += 32) {
+        const int at = (int)~(uint32_t)sm.cand[i];
+        const A w = weight(value_of((uint32_t)(sm.cand[i] >> 32)));
+        if (at >= r.seg0 && at < r.seg1 && w >= wmin) add += w;
+        if (!EXACT && use_m) open = open || fabs((double)w - (double)wmin) <= (double)wmin * 1e-5;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+      mass += add;
+    }
+    __syncthreads();
+  }
+  if (!good) {
+    if constexpr (EXACT) {
+      const Filter f{q.use_k ? q.k : 0, tp};
+      cutcode = cut_by_bisection<NT>(r, f, we, sm);
+      mass = 0;
+      walk<1>(r, [&](int j, float l) {
+        if (!(l > -INFINITY) || code_of(l, j) < cutcode) return;
+        const int64_t w = we(l);
+        mass += w >= wmin ? w : 0;
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      __syncthreads();
+    } else {
+      return false;
+    }
+  }
+  if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = mass;
+  if constexpr (!EXACT) {
+    if (!q.bins) e1 = block_reduce<NT>((double)s1, sm.red, Add{}, 0.0);
+    if (use_m && __syncthreads_or(open)) return false;
+  }
+  __syncthreads();
+  // the segment that holds the token (every warp finds it), then the warp's share of it
+  const A sv = lane < NW ? *reinterpret_cast<const A*>(&sm.seg[lane]) : A(0), sc = warp_scan(sv);
+  const A total = __shfl_sync(0xffffffffu, sc, 31);
+  const double target = (u > 0.0f ? (double)u : 0.0) * (double)total;
+  const bool last = EXACT && target >= (double)total;  // u >= 1: the last kept token
+  // fp32: what a sum may be off by, with the target's own error (all tokens' mass bounds the kept ones')
+  const double slack = EXACT ? 0.0 : 2.0 * (Expo32::kErr * (double)(q.bins ? z_all : total) - Expo32::kErrY * e1);
+  auto kept = [&](int j, int end) -> A {
+    if (j < r.off || j >= end) return A(0);
+    const float l = r.base[j];
+    if (!(l > -INFINITY) || code_of(l, j) < cutcode) return A(0);
+    const A w = weight(l);
+    return w >= wmin ? w : A(0);
+  };
+  const uint32_t has = __ballot_sync(0xffffffffu, sv > A(0) && (last || (double)sc > target));
+  if (!EXACT && !has) return false;
+  const int s = last ? 31 - __clz(has) : __ffs(has) - 1;
+  const A before = __shfl_sync(0xffffffffu, sc - sv, s);
+  const int sub = (r.per + NT - 1) / NT * 32;  // positions a warp
+  const int s0 = s * r.per + warp * sub, s1_ = min(min(s0 + sub, (s + 1) * r.per), r.end);
+  A part = 0;
+  for (int j = s0; j < s1_; j += 32) part += kept(j + lane, s1_);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+  __syncthreads();
+  if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = part;
+  if (tid == 0) sm.pick = 0;
+  __syncthreads();
+  const A pv = lane < NW ? *reinterpret_cast<const A*>(&sm.seg[lane]) : A(0), pc = warp_scan(pv);
+  const uint32_t at = __ballot_sync(0xffffffffu, pv > A(0) && (last || (double)(before + pc) > target));
+  const int owner = at ? (last ? 31 - __clz(at) : __ffs(at) - 1) : -1;
+  A run = before + __shfl_sync(0xffffffffu, pc - pv, warp);
+  if (warp == owner) {
+    int pick = -1;
+    for (int j = s0; j < s1_; j += 32) {
+      const A w = kept(j + lane, s1_), cum = warp_scan(w);
+      const uint32_t hit = __ballot_sync(0xffffffffu, w > A(0) && (last || (double)(run + cum) > target));
+      if (hit) {
+        const int h = last ? 31 - __clz(hit) : __ffs(hit) - 1;
+        pick = j + h;
+        if (!EXACT) {
+          // the token's borders; the first token's lower and the last one's upper are certain
+          const double up = (double)__shfl_sync(0xffffffffu, run + cum, h),
+                       down = (double)__shfl_sync(0xffffffffu, run + cum - w, h);
+          if (!(up - target > slack) || !(target - down > slack)) pick = -1;
+        }
+        if (!last) break;
+      }
+      run += __shfl_sync(0xffffffffu, cum, 31);
+    }
+    if (lane == 0 && pick >= 0) {
+      const float l = r.base[pick];
+      p.tokens[row] = pick - r.off;
+      if (p.logprob) {
+        const double z = EXACT ? log((double)total) - (double)p.sh * 0.6931471805599453 : log((double)total);
+        p.logprob[row] = (float)((l == q.mx ? 0.0 : ((double)l - (double)q.mx) / (double)T) - z);
+      }
+      sm.pick = 1;
+    }
+  }
+  if constexpr (EXACT) return true;
+  __syncthreads();
+  return sm.pick != 0;
+}
+
+// One CTA a row.  STAGED: the row is kept in shared memory after its first pass.
+template <int NT, bool STAGED>
+__global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
+  __shared__ Smem<NT> sm;
+  extern __shared__ __align__(16) float staged[];
+  constexpr int NW = NT / 32;
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float* x = p.logits + (int64_t)row * p.ld;
-  const int V = p.V, sh = p.sh;
+  Row r;
+  r.off = (int)((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
+  r.base = x - r.off;
+  r.end = r.off + p.V;
+  r.per = ((r.end + NW - 1) / NW + 127) / 128 * 128;
+  r.seg0 = min(warp * r.per, r.end);
+  r.seg1 = min(r.seg0 + r.per, r.end);
+  if (tid < 32) sm.tab[tid] = kExp2[tid];
+  const int sh = p.sh;
+  const float T = p.temperature ? p.temperature[row] : 1.0f;
+  const float u = p.u[row];
+  int k = p.top_k ? p.top_k[row] : 0;
+  const float tp = p.top_p ? p.top_p[row] : 1.0f;
+  const float mp = p.min_p ? p.min_p[row] : 0.0f;
 
-  // the largest logit, its lowest index
-  uint64_t best = 0;
-  for (int i = tid; i < V; i += kThreads) {
-    const uint64_t e = ((uint64_t)key_of(x[i]) << 32) | (uint32_t)~i;
-    best = e > best ? e : best;
+  // maximum (the row's, and the smallest of the threads'), lowest logit above -inf
+  float my_max = -INFINITY, mn = INFINITY;
+  walk4<STAGED ? 8 : 4>(r, [&](int j, const float4& v) {
+    if (STAGED) *reinterpret_cast<float4*>(staged + j) = v;
+    my_max = fmaxf(my_max, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));  // ignores NaN
+    if (v.x > -INFINITY) mn = fminf(mn, v.x);
+    if (v.y > -INFINITY) mn = fminf(mn, v.y);
+    if (v.z > -INFINITY) mn = fminf(mn, v.z);
+    if (v.w > -INFINITY) mn = fminf(mn, v.w);
+  });
+  float mx = my_max, mm = my_max > -INFINITY ? my_max : INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mm = fminf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
-  best = block_reduce(best, reinterpret_cast<uint64_t*>(red), MaxU64{});
-  const uint32_t kmax = (uint32_t)(best >> 32);
-  const int arg = (int)~(uint32_t)best;
-  if (kmax <= key_of(-INFINITY)) {  // nothing can be sampled: every logit is -inf or NaN
+  if (lane == 0) {
+    sm.redf[0][warp] = mx;
+    sm.redf[1][warp] = mm;
+    sm.redf[2][warp] = mn;
+  }
+  for (int i = tid; i < kTopBins; i += NT) sm.h.cnt[i] = 0u;
+  if (tid == 0) sm.ncand = 0;
+  __syncthreads();
+  mx = lane < NW ? sm.redf[0][lane] : -INFINITY;
+  mm = lane < NW ? sm.redf[1][lane] : INFINITY;
+  mn = lane < NW ? sm.redf[2][lane] : INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mm = fminf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+  }
+  if (STAGED) r.base = staged;
+  if (mx == -INFINITY) {  // nothing can be sampled
     if (tid == 0) {
       p.tokens[row] = -1;
       if (p.logprob) p.logprob[row] = -INFINITY;
     }
     return;
   }
-  const float mx = value_of(kmax);
-  const float T = p.temperature ? p.temperature[row] : 1.0f;
   if (!(T > 0.0f)) {  // greedy
+    int at = INT_MAX;
+    if (my_max == mx)
+      walk<4>(r, [&](int j, float l) {
+        if (l == mx) at = min(at, j);
+      });
+    at = block_reduce<NT>(at, sm.red, Min{}, INT_MAX);
     if (tid == 0) {
-      p.tokens[row] = arg;
+      p.tokens[row] = at - r.off;
       if (p.logprob) p.logprob[row] = 0.0f;
     }
     return;
   }
-  const double c = 1.4426950408889634 / (double)T;
-  const int k = p.top_k ? p.top_k[row] : 0;
-  const float tp = p.top_p ? p.top_p[row] : 1.0f;
-  const float mp = p.min_p ? p.min_p[row] : 0.0f;
-  // kept: key > cut, and of those with key == cut the first `ties` in index order
-  uint32_t cut = 0;
-  int64_t ties = V;
-  if (k > 0 && k < V) {
-    // the largest key with at least k elements at or above it
-    uint32_t lo = 0, hi = kmax;
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2 + 1;
-      int64_t n = 0;
-      for (int i = tid; i < V; i += kThreads) n += key_of(x[i]) >= mid;
-      n = block_reduce(n, red, Add{});
-      if (n >= k)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    cut = lo;
-    int64_t above = 0;
-    for (int i = tid; i < V; i += kThreads) above += key_of(x[i]) > cut;
-    ties = k - block_reduce(above, red, Add{});
-  }
-  if (!(tp >= 1.0f)) {
-    // mass of the first top_k; ties weigh the same
-    int64_t z = 0;
-    for (int i = tid; i < V; i += kThreads)
-      if (key_of(x[i]) > cut) z += weight_of(x[i], mx, c, sh);
-    z = block_reduce(z, red, Add{});
-    int64_t nt = 0;
-    for (int i = tid; i < V; i += kThreads) nt += key_of(x[i]) == cut;
-    nt = block_reduce(nt, red, Add{});
-    z += (nt < ties ? nt : ties) * weight_of(value_of(cut), mx, c, sh);
-    const double want = (tp > 0.0f ? (double)tp : 0.0) * (double)z;
-    // the smallest key whose predecessors (larger keys) have less than `want`
-    uint32_t lo = cut, hi = kmax;
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      int64_t s = 0;
-      for (int i = tid; i < V; i += kThreads)
-        if (key_of(x[i]) > mid) s += weight_of(x[i], mx, c, sh);
-      s = block_reduce(s, red, Add{});
-      if ((double)s < want)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    // of its ties, those whose predecessors have less than `want`
-    int64_t s = 0;
-    for (int i = tid; i < V; i += kThreads)
-      if (key_of(x[i]) > lo) s += weight_of(x[i], mx, c, sh);
-    s = block_reduce(s, red, Add{});
-    const int64_t w = weight_of(value_of(lo), mx, c, sh);
-    int64_t r = V;
-    if (w > 0) {
-      const double q = ceil((want - (double)s) / (double)w);
-      r = q < 1.0 ? 1 : (q > (double)V ? V : (int64_t)q);
-    }
-    ties = lo == cut ? (ties < r ? ties : r) : r;
-    cut = lo;
-  }
-  // min-p: a weight below it is dropped
+  const Expo weight(mx, T, sh, sm.tab);
   const int64_t wmin = mp > 0.0f ? __double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << sh)) : 0;
+  const bool use_p = !(tp >= 1.0f);
+  Cut q;
+  q.mx = mx;
+  q.scale = 0.0f;
 
-  // mass of every warp's segment
-  const int per = (V + kWarps - 1) / kWarps, a0 = warp * per, a1 = min(V, a0 + per);
-  int n = 0;
-  for (int i = a0 + lane; i < a1; i += 32) n += key_of(x[i]) == cut;
+  // A small top-k: the bin of the k-th largest of the threads' maxima holds, with
+  // the bins above it, at least k tokens and not many more, so one more pass
+  // collects them all.
+  if (k > 0 && k <= NT / 2) {
+    const float range = fminf(mx - mm, 128.0f);
+    q.scale = range > 0.0f ? fminf((float)(kTopBins - 1) / range, 1e30f) : 0.0f;
+    auto top_bin = [&](float l) { return fminf(q.fbin(l), Cut::kOne + (float)(kTopBins - 1)); };
+    if (my_max > -INFINITY) atomicAdd(&sm.h.cnt[__float_as_int(top_bin(my_max)) - 0x4b000000], 1u);
+    __syncthreads();
+    // every warp finds the bin
+    int c8[kTopBins / 32], sum = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  __syncthreads();
-  if (lane == 0) seg[warp] = n;
-  __syncthreads();
-  int64_t tie0 = 0;  // ties before this warp's segment
-  for (int w = 0; w < warp; ++w) tie0 += seg[w];
-  // weight of element i (0 where not kept); seen: ties before this lane's element
-  auto kept = [&](int i, int64_t& seen) -> int64_t {
-    const bool in = i < a1;
-    const float l = in ? x[i] : -INFINITY;
-    const uint32_t key = in ? key_of(l) : 0u;
-    const bool tie = in && key == cut;
-    const uint32_t bal = __ballot_sync(0xffffffffu, tie);
-    const int64_t before = seen + __popc(bal & ((1u << lane) - 1u));
-    seen += __popc(bal);
-    if (!in || !(key > cut || (tie && before < ties))) return 0;
-    const int64_t w = weight_of(l, mx, c, sh);
-    return w >= wmin ? w : 0;
-  };
-  int64_t mass = 0, seen = tie0;
-  for (int i = a0; i < a1; i += 32) mass += kept(i + lane, seen);
+    for (int e = 0; e < kTopBins / 32; ++e) {
+      sum += (int)sm.h.cnt[lane * (kTopBins / 32) + e];
+      c8[e] = sum;
+    }
+    const int64_t inc = warp_scan((int64_t)sum);
+    const int pre = (int)inc - sum;
+    int bstar = INT_MAX;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-  __syncthreads();
-  if (lane == 0) seg[warp] = mass;
-  __syncthreads();
-  int64_t total = 0, before = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += seg[w];
-    total += seg[w];
+    for (int e = kTopBins / 32 - 1; e >= 0; --e)
+      if (pre + c8[e] >= k) bstar = lane * (kTopBins / 32) + e;
+    bstar = __reduce_min_sync(0xffffffffu, bstar);
+    if (bstar < kTopBins - 1) {  // (the last bin takes in what is far below)
+      const float edge = Cut::kOne + (float)bstar;
+      walk<STAGED ? 2 : 4>(r, [&](int j, float l) {
+        if (!(l > -INFINITY) || !(top_bin(l) <= edge)) return;
+        const int at = atomicAdd(&sm.ncand, 1);
+        if (at < NT) sm.cand[at] = code_of(l, j);
+      });
+      __syncthreads();
+      const int n = sm.ncand;
+      if (n <= NT) {
+        pick_from_list<NT>(n, k, tp, -1, -1, wmin, u, weight, T, sm, p, row, r.off);
+        return;
+      }
+    }
+    __syncthreads();
   }
-  const float u = p.u[row];
-  const double target = (u > 0.0f ? (double)u : 0.0) * (double)total;
-  // u >= 1: the last kept token
-  const bool last = target >= (double)total;
-  const bool mine = last ? mass > 0 && before + mass == total
-                         : (double)before <= target && (double)(before + mass) > target;
-  if (!mine) return;  // one warp goes on
-  int64_t run = before;
-  seen = tie0;
-  int pick = -1;
-  for (int i = a0; i < a1; i += 32) {
-    int64_t w = kept(i + lane, seen), cum = w;
+
+  q.use_p = use_p;
+  q.use_k = k > 0;
+  if (q.use_k) {
+    int nf = 0;
+    walk<4>(r, [&](int, float l) { nf += l > -INFINITY; });
+    q.use_k = k < block_reduce<NT>((int64_t)nf, sm.red, Add{}, (int64_t)0);
+  }
+  q.k = q.use_k ? k : 0;
+  q.bins = q.use_k || use_p;
+  q.b1 = q.b2 = q.bk = kBins;
+  q.n1 = q.cnt_above = q.cnt_bk = 0;
+  q.fits = true;
+  if (q.bins) {
+    const float range = fminf(mx - mn, 128.0f);  // what is farther shares the last bin
+    q.scale = range > 0.0f ? fminf((float)(kBins - 1) / range, 1e30f) : 0.0f;
+    for (int i = tid; i < kBins; i += NT) sm.h.cnt[i] = sm.h.lo[i] = sm.h.hi[i] = 0u;
+    if (tid == 0) {
+      sm.ncand = 0;
+      sm.bk = sm.b1 = sm.b2 = kBins - 1;
+      sm.cnt_bk = 0;
+    }
+    __syncthreads();
+    const float c32 = weight.c32, unit = (float)(1u << (2 * p.half));
+    walk<2>(r, [&](int, float l) {
+      if (!(l > -INFINITY)) return;
+      const int b = q.bin(l);
+      atomicAdd(&sm.h.cnt[b], 1u);
+      if (use_p) {  // to within 1e-4 here; the cut itself is exact
+        float w;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((l - mx) * c32));
+        const uint32_t m = l == mx ? 1u << (2 * p.half) : (uint32_t)(w * unit);
+        if (m) {
+          atomicAdd(&sm.h.lo[b], m & ((1u << p.half) - 1u));
+          if (m >> p.half) atomicAdd(&sm.h.hi[b], m >> p.half);
+        }
+      }
+    });
+    __syncthreads();
+    constexpr int BPT = kBins / NT;  // bins a thread
+    int64_t cn[BPT], ms[BPT], cs = 0, mass = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, cum, o);
-      if (lane >= o) cum += t;
+    for (int e = 0; e < BPT; ++e) {
+      const int b = tid * BPT + e;
+      cs += sm.h.cnt[b];
+      mass += ((int64_t)sm.h.hi[b] << p.half) + sm.h.lo[b];
+      cn[e] = cs;
+      ms[e] = mass;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, w > 0 && (last || (double)(run + cum) > target));
-    if (hit) {
-      pick = i + (last ? 31 - __clz(hit) : __ffs(hit) - 1);
-      if (!last) break;
+    const int64_t c0 = block_scan<NT>(cs, sm.red) - cs;
+    int64_t m0 = 0, m_all = 0;
+    if (use_p) {
+      m0 = block_scan<NT>(mass, sm.red) - mass;
+      if (tid == NT - 1) sm.seg[0] = sm.seg[1] = m0 + mass;
+      __syncthreads();
+      m_all = sm.seg[0];
     }
-    run += __shfl_sync(0xffffffffu, cum, 31);
+    // sm.seg[0, 1]: mass before and with the last bin that counts
+    __syncthreads();
+    if (q.use_k) {
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) {
+        const int64_t pre = c0 + (e ? cn[e - 1] : 0);
+        if (pre < k && c0 + cn[e] >= k) {
+          sm.bk = tid * BPT + e;
+          sm.cnt_bk = (int)pre;
+          sm.seg[0] = m0 + (e ? ms[e - 1] : 0);
+          sm.seg[1] = m0 + ms[e];
+        }
+      }
+      __syncthreads();
+      q.bk = sm.bk;
+      q.cnt_bk = sm.cnt_bk;
+    }
+    const int last = q.use_k ? q.bk : kBins - 1;
+    if (use_p) {
+      // a bin's true mass is between m and m + its tokens (truncated units), to 1e-4
+      const double pp = tp > 0.0f ? (double)tp : 0.0;
+      const double w_lo = pp * (double)sm.seg[0] * 0.9998 - (double)p.V,
+                   w_hi = pp * ((double)sm.seg[1] + p.V) * 1.0002 + 1.0;
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) {
+        const int b = tid * BPT + e;
+        const double cum = (double)(m0 + ms[e]), pre = (double)(m0 + (e ? ms[e - 1] : 0));
+        // the first bin that may, and the first that must, reach what is wanted
+        if (cum + p.V >= w_lo && (b == 0 || pre + p.V < w_lo)) sm.b1 = b;
+        if (cum >= w_hi && (b == 0 || pre < w_hi)) sm.b2 = b;
+      }
+      __syncthreads();
+      q.b1 = min(sm.b1, last);
+      q.b2 = min(sm.b2, last);
+    } else {
+      q.b1 = q.b2 = q.bk;
+    }
+#pragma unroll
+    for (int e = 0; e < BPT; ++e) {
+      const int b = tid * BPT + e;
+      if (b == q.b1) sm.cnt_b1 = (int)(c0 + (e ? cn[e - 1] : 0));
+      if (b == q.b2) sm.cnt_b2 = (int)(c0 + cn[e]);
+    }
+    __syncthreads();
+    q.cnt_above = sm.cnt_b1;
+    q.n1 = sm.cnt_b2 - q.cnt_above;
+    const int in_bk = q.use_k ? (int)sm.h.cnt[q.bk] : 0;
+    q.fits = q.n1 + (q.use_k && q.bk > q.b2 ? in_bk : 0) <= NT;
+    __syncthreads();
+    if (!q.use_k && q.cnt_above + q.n1 <= kListMax) {
+      // A small nucleus: all its tokens fit the list, and the mass from the
+      // histogram (fp32 weights: off by less than 6e-6 and a unit a token) settles
+      // the cut unless it falls that close to a token's border.
+      const float edge = Cut::kOne + (float)q.b2;
+      walk<STAGED ? 2 : 4>(r, [&](int j, float l) {
+        if (l > -INFINITY && q.fbin(l) <= edge) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l, j);
+      });
+      const double per = exp2((double)(sh - 2 * p.half));
+      const int64_t z_lo = (int64_t)((double)m_all * per * (1.0 - 6e-6)),
+                    z_hi = (int64_t)(((double)m_all + p.V) * per * (1.0 + 6e-6)) + 1;
+      __syncthreads();
+      if (pick_from_list<NT>(q.cnt_above + q.n1, INT_MAX, tp, z_lo, z_hi, wmin, u, weight, T, sm, p, row, r.off))
+        return;
+      __syncthreads();
+    }
   }
-  if (lane == 0) {
-    p.tokens[row] = pick;
-    if (p.logprob) {
-      const double z = log((double)total) - (double)sh * 0.6931471805599453;
-      p.logprob[row] = (float)((x[pick] == mx ? 0.0 : ((double)x[pick] - (double)mx) / (double)T) - z);
-    }
+  if (q.fits && u < 1.0f && Expo32::usable(mx, T)) {
+    if (pick_from_row<NT, false>(r, q, tp, mp, u, T, weight, sm, p, row)) return;
+    __syncthreads();
   }
+  pick_from_row<NT, true>(r, q, tp, mp, u, T, weight, sm, p, row);
+}
+
+template <int NT, bool STAGED>
+nc_status launch_t(const SampleParams& p, int M, size_t smem, cudaStream_t stream) {
+  auto* fn = sample_kernel<NT, STAGED>;
+  if (smem > 0 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return NC_ERR_CUDA;
+  fn<<<M, NT, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
 }
 
 }  // namespace
@@ -279,9 +987,14 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   int bits = 0;  // V <= 2^bits
   while (((int64_t)1 << bits) < V) ++bits;
   const int sh = 62 - bits < 51 ? 62 - bits : 51;
-  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh};
-  sample_kernel<<<M, kThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
+  const int half = 31 - bits < 15 ? 31 - bits : 15;  // V tokens in one bin do not overflow a sum
+  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, half};
+  // Rows for every SM and more: two a SM, one loads while the other computes (from
+  // L2 after its first pass).  Fewer: a row's later passes from shared memory.
+  if (M > device_sm_count()) return launch_t<512, false>(p, M, 0, stream);
+  const size_t smem = ((size_t)V + 7) / 4 * 16;
+  if (smem <= 160 * 1024) return launch_t<1024, true>(p, M, smem, stream);
+  return launch_t<1024, false>(p, M, 0, stream);
 }
 
 }  // namespace nc

@@ -251,6 +251,33 @@ def test_sample_ties_and_extremes(gpu):
     _check_sample(l, u, tok, lp, T)
 
 
+@pytest.mark.parametrize("V,M", [(300000, 2), (1 << 20, 1), (140001, 3), (32749, 300)])
+def test_sample_large_vocabularies_and_many_rows(gpu, V, M):
+    rng = np.random.default_rng(V)
+    l = (1.5 * rng.standard_normal((M, V)) + rng.exponential(1.2, (M, V))).astype(np.float32)
+    u = rng.random(M).astype(np.float32)
+    for kw in [{}, dict(top_k=np.full(M, 40)), dict(top_p=np.full(M, 0.9)), dict(top_k=np.full(M, 20000), top_p=np.full(M, 0.8)),
+               dict(top_k=np.full(M, 3000), min_p=np.full(M, 0.05))]:
+        tok, lp = _sample(gpu, l, u, **kw)
+        _check_sample(l, u, tok, lp, **kw)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.01, 1.0, 30.0, 1e4])
+def test_sample_logits_of_any_spread(gpu, scale):
+    """Logits packed into few histogram bins, or spread far past them."""
+    rng = np.random.default_rng(4)
+    M, V = 4, 20011
+    l = (scale * rng.standard_normal((M, V))).astype(np.float32)
+    l[2] = np.round(l[2] / scale) * np.float32(scale)   # about ten values: thousands of ties
+    l[3, ::3] = -3e38
+    u = rng.random(M).astype(np.float32)
+    for T in (1.0, scale):
+        for kw in [{}, dict(top_k=np.array([1, 1500, 4000, 12000])), dict(top_p=np.array([0.1, 0.5, 0.9, 0.999])),
+                   dict(top_k=np.full(M, 9000), top_p=np.full(M, 0.6)), dict(top_k=np.full(M, 50), top_p=np.full(M, 0.95), min_p=np.full(M, 0.1))]:
+            tok, lp = _sample(gpu, l, u, temperature=np.full(M, T), **kw)
+            _check_sample(l, u, tok, lp, np.full(M, T), **kw)
+
+
 def test_sample_strided_rows_and_no_logprob(gpu):
     x = torch.randn((5, 4, 777), device=DEV)
     l = x[:, 2]

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "nc_internal.h"
+#include "nc_ptx.cuh"
 
 namespace nc {
 namespace {
@@ -80,9 +81,9 @@ struct Expo {
   int shx;               // sh << 20
   const double* tab;     // kExp2 in shared memory
 
-  __device__ Expo(float mx_, float T, int sh, const double* tab_)
-      : mx(mx_), c32((float)(1.4426950408889634 / (double)T)), least(-(float)(sh + 1)),
-        mxd(mx_ == INFINITY ? 0.0 : (double)mx_), c(1.4426950408889634 / (double)T), shx(sh << 20), tab(tab_) {}
+  __device__ Expo(float mx_, double c_, int sh, const double* tab_)
+      : mx(mx_), c32((float)c_), least(-(float)(sh + 1)), mxd(mx_ == INFINITY ? 0.0 : (double)mx_), c(c_),
+        shx(sh << 20), tab(tab_) {}
 
   static constexpr int64_t kRaw0 = 0x4330000000000000ll;  // the bits of 2^52: what 0 looks like
 
@@ -118,12 +119,12 @@ struct Expo32 {
   // makes the difference's low part inexact, 2^-24 |y| ln 2; sums of four add
   // three times 2^-24.
   static constexpr double kErr = 5e-7, kErrY = 4.5e-8;
+  static constexpr double kHist = 2e-6;  // the two for |y| < 31: a sum of weights from 2^-30 on
 
-  __device__ Expo32(float mx_, float T) : mx(mx_) {
-    const double c = 1.4426950408889634 / (double)T;
+  __device__ Expo32(float mx_, double c, float T) : mx(mx_) {
     c_hi = (float)c;
     c_lo = (float)(c - (double)c_hi);
-    least = mx_ - (float)(100.0 / c);  // below it a weight is 2^-100: nothing beside 1
+    least = mx_ - 69.3f * T;  // below it a weight is 2^-100: nothing beside 1
   }
   __device__ static bool usable(float mx, float T) {
     return T > 1e-20f && T < 1e20f && fabsf(mx) < 1e5f * T;
@@ -186,19 +187,74 @@ __device__ __forceinline__ void walk(const Row& r, F f) {
   });
 }
 
+// f(position, logit) says whether a token is listed; every warp keeps the first
+// kOwn of its own in its part of `own`, without an atomic (the same counter for
+// all costs about a hundred cycles a token), and puts them into list[] at the end.
+// Returns how many there are (list holds the first cap).  For the whole block.
+template <int NT, int U, typename F>
+__device__ __forceinline__ int collect(const Row& r, uint64_t* own, uint64_t* list, int cap, int* total, F f) {
+  constexpr int kOwn = 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n = 0;  // the warp's
+  uint64_t* mine = own + warp * kOwn;
+  __syncthreads();
+  if (threadIdx.x == 0) *total = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int j0 = r.seg0; j0 < r.seg1; j0 += 128 * U) {
+    float4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int j = j0 + k * 128 + lane * 4;
+      v[k] = j < r.seg1 ? load4(r, j) : make_float4(NAN, NAN, NAN, NAN);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int j = j0 + k * 128 + lane * 4;
+      const bool t0 = f(v[k].x), t1 = f(v[k].y), t2 = f(v[k].z), t3 = f(v[k].w);
+      if (!__any_sync(0xffffffffu, t0 || t1 || t2 || t3)) continue;
+      const float l[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      const bool t[4] = {t0, t1, t2, t3};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bal = __ballot_sync(0xffffffffu, t[e]);
+        const int at = n + __popc(bal & ((1u << lane) - 1u));
+        if (t[e]) {
+          const uint64_t code = ((uint64_t)key_of(l[e]) << 32) | (uint32_t)~(j + e);
+          if (at < kOwn) {
+            mine[at] = code;
+          } else {
+            const int g = atomicAdd(total, 1);
+            if (g < cap) list[g] = code;
+          }
+        }
+        n += __popc(bal);
+      }
+    }
+  }
+  const int keep = min(n, kOwn);
+  int base = 0;
+  if (lane == 0) base = atomicAdd(total, keep);
+  base = __shfl_sync(0xffffffffu, base, 0);
+  __syncwarp();
+  for (int i = lane; i < keep; i += 32)
+    if (base + i < cap) list[base + i] = mine[i];
+  __syncthreads();
+  return *total;
+}
+
 // Order of the tokens: larger first (logit, then lower index).
 __device__ __forceinline__ uint64_t code_of(float l, int pos) {
   return ((uint64_t)key_of(l) << 32) | (uint32_t)~pos;
 }
 
 constexpr int kTopBins = 256;  // histogram of the threads' maxima
-constexpr int kListMax = 256;  // nuclei of more tokens than this are not listed whole
 
 template <int NT>
 struct Smem {
-  double tab[32];
+  double tab[32], c;  // log2(e) / T
   int64_t red[32];
-  float redf[3][32];
+  float redf[2][32];
   int64_t seg[32];
   union {
     struct {
@@ -211,6 +267,8 @@ struct Smem {
     } s;
   };
   uint64_t cand[NT];
+  uint64_t own[NT * 2];
+  uint64_t bar[NT / 32];
   int ncand, bk, cnt_bk, b1, b2, cnt_b1, cnt_b2, pick;
 };
 
@@ -219,6 +277,9 @@ struct Add {
   __device__ T operator()(T a, T b) const {
     return a + b;
   }
+};
+struct MinF {
+  __device__ float operator()(float a, float b) const { return fminf(a, b); }
 };
 struct Min {
   __device__ int operator()(int a, int b) const { return min(a, b); }
@@ -273,7 +334,7 @@ struct Filter {
 // over the keys, a pass of the row each.  For rows whose cut falls among more
 // more tokens of one bin than the block has threads (heavy ties, logits spread over hundreds).
 template <int NT>
-__device__ __noinline__ uint64_t cut_by_bisection(const Row& r, const Filter& f, const Expo& weight, Smem<NT>& sm) {
+__device__ __noinline__ uint64_t cut_by_bisection(const Row r, const Filter f, const Expo weight, Smem<NT>& sm) {
   const uint32_t kmax = key_of(weight.mx);
   uint32_t cut = 0;
   int64_t ties = INT_MAX;
@@ -392,7 +453,7 @@ __device__ __forceinline__ int pow2_from(int n) { return n <= 1 ? 1 : 1 << (32 -
 // the cut.  Called by the whole block.
 template <int NT>
 __device__ __noinline__ bool pick_from_list(int n, int k, float tp, int64_t z_lo, int64_t z_hi, int64_t wmin, float u,
-                                            const Expo& weight, float T, Smem<NT>& sm, const SampleParams& p, int row,
+                                            const Expo weight, float T, Smem<NT>& sm, const SampleParams& p, int row,
                                             int off) {
   const int tid = threadIdx.x;
   const bool use_p = !(tp >= 1.0f);
@@ -411,7 +472,9 @@ __device__ __noinline__ bool pick_from_list(int n, int k, float tp, int64_t z_lo
   // top-p and min-p keep a first part of the order as well
   bool keep = tid < n && w >= wmin;
   if (use_p) {
-    if (__syncthreads_or(keep && tid > 0 && b >= pp * (double)z_lo && b < pp * (double)z_hi)) return false;
+    const bool open = (keep && tid > 0 && b >= pp * (double)z_lo && b < pp * (double)z_hi) ||
+                      (tid == n - 1 && (double)cum < pp * (double)z_hi);  // the cut may lie past the list
+    if (__syncthreads_or(open)) return false;
     keep = keep && (tid == 0 || b < pp * (double)z_lo);
   }
   n = __syncthreads_count(keep);
@@ -448,15 +511,15 @@ struct Cut {
   int k, b1, b2, bk;  // top-k's bin; the bracket of top-p's (without it: bk twice)
   int n1, cnt_above, cnt_bk;  // tokens in the bracket, before it, before bk
   bool fits;  // the tokens of the bracket and of bk can be sorted
+  double z_lo, z_hi;  // bounds of all tokens' mass (top-p)
 
-  // Rounded to the nearest bin: never falls where l grows down, which is all that
-  // is asked of it; a float, so comparing needs no conversion.
+  // Rounded to the nearest bin: never falls where l falls, which is all that is
+  // asked of it; a float, so comparing needs no conversion.  Not clamped to the
+  // last bin, kFar; NaN stays NaN.
   static constexpr float kOne = 8388608.0f;  // 2^23: the sum's last bit is 1
-  __device__ __forceinline__ float fbin(float l) const {
-    const float d = l == mx ? 0.0f : mx - l;
-    return fminf(fmaf(d, scale, kOne), kOne + (float)(kBins - 1));
-  }
-  __device__ __forceinline__ int bin(float l) const { return __float_as_int(fbin(l)) - 0x4b000000; }
+  static constexpr float kFar = kOne + (float)(kBins - 1);
+  __device__ __forceinline__ float fbin(float l) const { return fmaf(mx - l, scale, kOne); }
+  __device__ __forceinline__ int bin(float l) const { return __float_as_int(fminf(fbin(l), kFar)) - 0x4b000000; }
 };
 
 // The row's token from its bracket: a pass that sums every segment's sure tokens
@@ -464,14 +527,15 @@ struct Cut {
 // share of it and the token.  EXACT: integer weights (and, if the bracket fails,
 // the bisection); else fp32 ones, false where their error leaves it open.
 template <int NT, bool EXACT>
-__device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp, float mp, float u, float T,
-                                           const Expo& we, Smem<NT>& sm, const SampleParams& p, int row) {
+__device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, float mp, float u, float T,
+                                           const Expo we, Smem<NT>& sm, const SampleParams& p, int row) {
   using A = typename std::conditional<EXACT, int64_t, double>::type;
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Expo32 wf(q.mx, T);
-  const A wmin = EXACT ? (A)(mp > 0.0f ? __double2ll_ru((double)fminf(mp, 1.0f) * exp2((double)p.sh)) : 0)
-                       : (A)(mp > 0.0f ? fminf(mp, 1.0f) : 0.0f);
+  const Expo32 wf(q.mx, we.c, T);
+  A wmin = 0;
+  if (mp > 0.0f)
+    wmin = EXACT ? (A)__double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << p.sh)) : (A)fminf(mp, 1.0f);
   const bool use_m = mp > 0.0f;
   // a token's weight; fp32: its share of the error bound, and whether min-p is open
   float s1 = 0.0f;
@@ -490,7 +554,12 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
     if (fmaxf(fmaxf(a, b), fmaxf(c, d)) > 0.004f) return ((double)a + (double)b) + ((double)c + (double)d);
     return (double)((a + b) + (c + d));
   };
-  const float f1 = Cut::kOne + (float)q.b1, f2 = Cut::kOne + (float)q.b2, fk = Cut::kOne + (float)q.bk;
+  // a bin as a bound of fbin: with top-k the last one took in all beyond it
+  auto upto = [&](int b) { return q.use_k && b >= kBins - 1 ? INFINITY : Cut::kOne + (float)b; };
+  const float f1 = Cut::kOne + (float)q.b1, f2 = upto(q.b2), fk = Cut::kOne + (float)q.bk, fk2 = upto(q.bk);
+  auto listed = [&](float l, float b) {
+    return l > -INFINITY && ((b >= f1 && b <= f2) || (q.use_k && b >= fk && b <= fk2));
+  };
   if (tid == 0) sm.ncand = 0;
   __syncthreads();
   bool good = q.fits;
@@ -505,16 +574,25 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
         sum -= (uint64_t)(lane0 < r.seg1 ? (r.seg1 - lane0 + 127) / 128 * 4 : 0) * (uint64_t)Expo::kRaw0;
         mass = (A)sum;
       } else {
+        const float f_rest = q.use_k ? fk : INFINITY;  // top-p's mass ends before it
         walk<1>(r, [&](int j, float l) {
           const int64_t w = we(l);
+          if (!q.bins) {
+            mass += w >= wmin ? w : 0;
+            return;
+          }
           const float b = q.fbin(l);
-          const bool cand = q.bins && l > -INFINITY && b >= f1 && (b <= f2 || (q.use_k && b == fk));
-          const bool sure = !q.bins || b < f1;
-          if (cand) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l, j);
-          za += sure ? w : 0;
-          zt += !cand && (!q.use_k || b < fk) ? w : 0;
-          mass += sure && w >= wmin ? w : 0;
+          if (b < f1) {
+            za += w;
+            if (use_m) mass += w >= wmin ? w : 0;
+          } else if (listed(l, b)) {
+            sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l, j);
+          } else if (b < f_rest) {
+            zt += w;
+          }
         });
+        zt += za;
+        if (q.bins && !use_m) mass = za;
       }
     } else if (!q.bins) {
       walk4<4>(r, [&](int, const float4& v) {
@@ -533,29 +611,38 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
         mass += sum4(w0, w1, w2, w3);
       });
     } else {
+      // tokens past the bracket (with top-k: past its bin) need no weight: without
+      // top-k, top-p's mass comes from the histogram
+      const float fl = q.use_k ? fk2 : f2;
       walk4<2>(r, [&](int j, const float4& v) {
         const float l[4] = {v.x, v.y, v.z, v.w};
-        float a[4], t[4], m[4];
+        const float b[4] = {q.fbin(v.x), q.fbin(v.y), q.fbin(v.z), q.fbin(v.w)};
+        if (!(fminf(fminf(b[0], b[1]), fminf(b[2], b[3])) <= fl)) return;  // NaN gives way to the others
+        float a[4], t[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float y;
-          const float w = wf(l[e], y), b = q.fbin(l[e]);
+          const float w = wf(l[e], y);
           s1 = fmaf(w, y, s1);
-          const bool cand = l[e] > -INFINITY && b >= f1 && (b <= f2 || (q.use_k && b == fk));
-          const bool sure = b < f1;
-          if (cand) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l[e], j + e);
-          a[e] = sure ? w : 0.0f;
-          t[e] = !cand && (!q.use_k || b < fk) ? w : 0.0f;
-          m[e] = a[e];
-          if (use_m) {
-            open = open || fabsf(w - (float)wmin) <= (float)wmin * 1e-5f;
-            m[e] = w >= (float)wmin ? a[e] : 0.0f;
-          }
+          a[e] = b[e] < f1 ? w : 0.0f;
+          t[e] = b[e] > f2 && b[e] < fk ? w : 0.0f;
+          if (!(b[e] < f1) && listed(l[e], b[e])) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l[e], j + e);
         }
         const double a4 = sum4(a[0], a[1], a[2], a[3]);
         za += a4;
-        zt += sum4(t[0], t[1], t[2], t[3]);
-        mass += use_m ? sum4(m[0], m[1], m[2], m[3]) : a4;
+        zt += a4;
+        if (q.use_k) zt += sum4(t[0], t[1], t[2], t[3]);
+        if (use_m) {
+          const float m = (float)wmin;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            open = open || fabsf(a[e] - m) <= m * 1e-5f;
+            a[e] = a[e] >= m ? a[e] : 0.0f;
+          }
+          mass += sum4(a[0], a[1], a[2], a[3]);
+        } else {
+          mass += a4;
+        }
       });
     }
 #pragma unroll
@@ -585,8 +672,10 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
       err = 2.0 * (Expo32::kErr * z_all - Expo32::kErrY * e1);
     }
     if (q.use_p) {
-      const double z = (double)(zt + (cut > 0 ? cums[cut - 1] : A(0)));
-      const double want = (tp > 0.0f ? (double)tp : 0.0) * z;
+      const double pp = tp > 0.0f ? (double)tp : 0.0, z = (double)(zt + (cut > 0 ? cums[cut - 1] : A(0)));
+      const bool range = !EXACT && !q.use_k;
+      const double want = pp * (range ? 0.5 * (q.z_lo + q.z_hi) : z);
+      if (range) err += pp * 0.5 * (q.z_hi - q.z_lo);
       int lo = 0, hi = min(q.n1, cut);  // candidates with less than `want` before them
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
@@ -597,7 +686,7 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
       }
       // the bracket holds the cut
       good = (q.cnt_above == 0 || (double)za < want) &&
-             (lo < q.n1 || q.b2 == (q.use_k ? q.bk : kBins - 1) ||
+             (lo < q.n1 || (q.use_k && q.b2 == q.bk) ||
               (q.n1 > 0 && (double)(za + cums[q.n1 - 1]) >= want));
       if (!EXACT && good) {  // and no token's border is within the error of what is wanted
         auto before = [&](int i) { return (double)(za + (i ? cums[i - 1] : A(0))); };
@@ -605,7 +694,7 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
           good = q.cnt_above == 0;
         else
           good = want - before(lo - 1) > err || (lo == 1 && q.cnt_above == 0);
-        if (lo < min(q.n1, cut) || (lo == q.n1 && q.b2 != (q.use_k ? q.bk : kBins - 1)))
+        if (lo < min(q.n1, cut) || (lo == q.n1 && !(q.use_k && q.b2 == q.bk)))
           good = good && before(lo) - want > err;
       }
       cut = q.cnt_above == 0 ? max(lo, 1) : lo;
@@ -717,7 +806,7 @@ __device__ __noinline__ bool pick_from_row(const Row& r, const Cut& q, float tp,
 
 // One CTA a row.  STAGED: the row is kept in shared memory after its first pass.
 template <int NT, bool STAGED>
-__global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const SampleParams p) {
   __shared__ Smem<NT> sm;
   extern __shared__ __align__(16) float staged[];
   constexpr int NW = NT / 32;
@@ -730,49 +819,71 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
   r.per = ((r.end + NW - 1) / NW + 127) / 128 * 128;
   r.seg0 = min(warp * r.per, r.end);
   r.seg1 = min(r.seg0 + r.per, r.end);
-  if (tid < 32) sm.tab[tid] = kExp2[tid];
   const int sh = p.sh;
   const float T = p.temperature ? p.temperature[row] : 1.0f;
+  if (tid < 32) sm.tab[tid] = kExp2[tid];
+  if (tid == 32) sm.c = 1.4426950408889634 / (double)T;
   const float u = p.u[row];
   int k = p.top_k ? p.top_k[row] : 0;
   const float tp = p.top_p ? p.top_p[row] : 1.0f;
   const float mp = p.min_p ? p.min_p[row] : 0.0f;
 
-  // maximum (the row's, and the smallest of the threads'), lowest logit above -inf
-  float my_max = -INFINITY, mn = INFINITY;
-  walk4<STAGED ? 8 : 4>(r, [&](int j, const float4& v) {
-    if (STAGED) *reinterpret_cast<float4*>(staged + j) = v;
+  // the maximum; the smallest of the threads' maxima
+  float my_max = -INFINITY;
+  bool late = false;  // the copy did not arrive
+  if (STAGED) {
+    // each warp's segment by one asynchronous copy of its own, the row's first and
+    // last few tokens (not whole 16 bytes) by plain loads
+    const int a = max(r.seg0, (r.off + 3) & ~3), b = min(r.seg1, r.end & ~3);
+    if (lane == 0) {
+      mbar_init(smem_u32(&sm.bar[warp]), 1);
+      fence_mbar_init();
+      if (a < b) {
+        mbar_arrive_expect_tx(smem_u32(&sm.bar[warp]), (uint32_t)(b - a) * 4);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_u32(staged + a)),
+                     "l"(r.base + a), "r"((b - a) * 4), "r"(smem_u32(&sm.bar[warp]))
+                     : "memory");
+      }
+    }
+    if (r.seg0 == 0 && lane >= r.off && lane < min(4, r.end)) staged[lane] = r.base[lane];
+    if (b < r.seg1 && lane < r.seg1 - b && b + lane >= r.off) staged[b + lane] = r.base[b + lane];
+    __syncwarp();
+    r.base = staged;
+    if (a < b) {
+      const uint64_t t0 = global_timer_ns();
+      while (!late && !mbar_try_wait(smem_u32(&sm.bar[warp]), 0)) late = global_timer_ns() - t0 > kWaitLimitNs;
+    }
+  }
+  walk4<4>(r, [&](int j, const float4& v) {
     my_max = fmaxf(my_max, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));  // ignores NaN
-    if (v.x > -INFINITY) mn = fminf(mn, v.x);
-    if (v.y > -INFINITY) mn = fminf(mn, v.y);
-    if (v.z > -INFINITY) mn = fminf(mn, v.z);
-    if (v.w > -INFINITY) mn = fminf(mn, v.w);
   });
   float mx = my_max, mm = my_max > -INFINITY ? my_max : INFINITY;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mm = fminf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
   if (lane == 0) {
     sm.redf[0][warp] = mx;
     sm.redf[1][warp] = mm;
-    sm.redf[2][warp] = mn;
   }
   for (int i = tid; i < kTopBins; i += NT) sm.h.cnt[i] = 0u;
   if (tid == 0) sm.ncand = 0;
-  __syncthreads();
+  if (__syncthreads_or(late)) {
+    if (tid == 0) {
+      p.tokens[row] = -1;
+      if (p.logprob) p.logprob[row] = NAN;
+    }
+    return;
+  }
   mx = lane < NW ? sm.redf[0][lane] : -INFINITY;
   mm = lane < NW ? sm.redf[1][lane] : INFINITY;
-  mn = lane < NW ? sm.redf[2][lane] : INFINITY;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mm = fminf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
-  if (STAGED) r.base = staged;
   if (mx == -INFINITY) {  // nothing can be sampled
     if (tid == 0) {
       p.tokens[row] = -1;
@@ -793,8 +904,9 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
     }
     return;
   }
-  const Expo weight(mx, T, sh, sm.tab);
-  const int64_t wmin = mp > 0.0f ? __double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << sh)) : 0;
+  const Expo weight(mx, sm.c, sh, sm.tab);
+  int64_t wmin = 0;
+  if (mp > 0.0f) wmin = __double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << sh));
   const bool use_p = !(tp >= 1.0f);
   Cut q;
   q.mx = mx;
@@ -803,11 +915,11 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
   // A small top-k: the bin of the k-th largest of the threads' maxima holds, with
   // the bins above it, at least k tokens and not many more, so one more pass
   // collects them all.
-  if (k > 0 && k <= NT / 2) {
+  if (k > 0 && k <= NT / 2 && mx < INFINITY) {
     const float range = fminf(mx - mm, 128.0f);
-    q.scale = range > 0.0f ? fminf((float)(kTopBins - 1) / range, 1e30f) : 0.0f;
-    auto top_bin = [&](float l) { return fminf(q.fbin(l), Cut::kOne + (float)(kTopBins - 1)); };
-    if (my_max > -INFINITY) atomicAdd(&sm.h.cnt[__float_as_int(top_bin(my_max)) - 0x4b000000], 1u);
+    q.scale = range > 0.0f ? fminf((float)(kTopBins - 1) / range, 1e30f) : 0.0f;  // 0: all the same
+    if (my_max > -INFINITY)
+      atomicAdd(&sm.h.cnt[__float_as_int(fminf(q.fbin(my_max), Cut::kOne + (float)(kTopBins - 1))) - 0x4b000000], 1u);
     __syncthreads();
     // every warp finds the bin
     int c8[kTopBins / 32], sum = 0;
@@ -824,14 +936,12 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
       if (pre + c8[e] >= k) bstar = lane * (kTopBins / 32) + e;
     bstar = __reduce_min_sync(0xffffffffu, bstar);
     if (bstar < kTopBins - 1) {  // (the last bin takes in what is far below)
-      const float edge = Cut::kOne + (float)bstar;
-      walk<STAGED ? 2 : 4>(r, [&](int j, float l) {
-        if (!(l > -INFINITY) || !(top_bin(l) <= edge)) return;
-        const int at = atomicAdd(&sm.ncand, 1);
-        if (at < NT) sm.cand[at] = code_of(l, j);
-      });
-      __syncthreads();
-      const int n = sm.ncand;
+      // a value at or below every one in the bins up to it (a little lower: it was
+      // fp32 arithmetic that put them there)
+      const float edge = mx - ((float)bstar + 0.51f) / q.scale - fabsf(mx) * 1e-6f;
+      const int n = q.scale > 0.0f ? collect<NT, 2>(r, sm.own, sm.cand, NT, &sm.ncand,
+                                                    [&](float l) { return l >= edge; })
+                                   : NT + 1;
       if (n <= NT) {
         pick_from_list<NT>(n, k, tp, -1, -1, wmin, u, weight, T, sm, p, row, r.off);
         return;
@@ -842,19 +952,33 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
 
   q.use_p = use_p;
   q.use_k = k > 0;
-  if (q.use_k) {
+  // Top-p alone: the histogram covers what weighs e^-8 and more, where the cut
+  // mostly is (the tail's mass is summed aside), or else down to 2^-32.
+  float spread = INFINITY;
+  if (q.use_k || T > 4.0f) {
     int nf = 0;
-    walk<4>(r, [&](int, float l) { nf += l > -INFINITY; });
-    q.use_k = k < block_reduce<NT>((int64_t)nf, sm.red, Add{}, (int64_t)0);
+    float mn = INFINITY;
+    walk<4>(r, [&](int, float l) {
+      if (l > -INFINITY) {
+        ++nf;
+        mn = fminf(mn, l);
+      }
+    });
+    q.use_k = q.use_k && k < block_reduce<NT>((int64_t)nf, sm.red, Add{}, (int64_t)0);
+    spread = mx - block_reduce<NT>(mn, sm.red, MinF{}, INFINITY);
   }
   q.k = q.use_k ? k : 0;
   q.bins = q.use_k || use_p;
   q.b1 = q.b2 = q.bk = kBins;
+  q.z_lo = q.z_hi = 0.0;
   q.n1 = q.cnt_above = q.cnt_bk = 0;
   q.fits = true;
-  if (q.bins) {
-    const float range = fminf(mx - mn, 128.0f);  // what is farther shares the last bin
+  if (q.bins && !(mx < INFINITY)) q.fits = false;
+  for (int turn = 0; q.bins && q.fits && turn < 2; ++turn) {
+    // with top-k, what is farther shares the last bin
+    const float range = q.use_k ? fminf(spread, 128.0f) : fminf(spread, (turn == 0 ? 8.0f : 22.5f) * T);
     q.scale = range > 0.0f ? fminf((float)(kBins - 1) / range, 1e30f) : 0.0f;
+    __syncthreads();
     for (int i = tid; i < kBins; i += NT) sm.h.cnt[i] = sm.h.lo[i] = sm.h.hi[i] = 0u;
     if (tid == 0) {
       sm.ncand = 0;
@@ -862,15 +986,18 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
       sm.cnt_bk = 0;
     }
     __syncthreads();
-    const float c32 = weight.c32, unit = (float)(1u << (2 * p.half));
-    walk<2>(r, [&](int, float l) {
+    const Expo32 wf(mx, sm.c, T);
+    const float unit = (float)(1u << (2 * p.half));
+    int64_t tail = 0;
+    walk<1>(r, [&](int, float l) {
       if (!(l > -INFINITY)) return;
-      const int b = q.bin(l);
-      atomicAdd(&sm.h.cnt[b], 1u);
-      if (use_p) {  // to within 1e-4 here; the cut itself is exact
-        float w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((l - mx) * c32));
-        const uint32_t m = l == mx ? 1u << (2 * p.half) : (uint32_t)(w * unit);
+      float y;
+      const uint32_t m = !use_p ? 0u : l == mx ? 1u << (2 * p.half) : (uint32_t)(wf(l, y) * unit);
+      if (!q.use_k && q.fbin(l) > Cut::kFar) {
+        tail += m;
+      } else {
+        const int b = q.bin(l);
+        atomicAdd(&sm.h.cnt[b], 1u);
         if (m) {
           atomicAdd(&sm.h.lo[b], m & ((1u << p.half) - 1u));
           if (m >> p.half) atomicAdd(&sm.h.hi[b], m >> p.half);
@@ -891,8 +1018,12 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
     const int64_t c0 = block_scan<NT>(cs, sm.red) - cs;
     int64_t m0 = 0, m_all = 0;
     if (use_p) {
+      tail = q.use_k ? 0 : block_reduce<NT>(tail, sm.red, Add{}, (int64_t)0);
       m0 = block_scan<NT>(mass, sm.red) - mass;
-      if (tid == NT - 1) sm.seg[0] = sm.seg[1] = m0 + mass;
+      if (tid == NT - 1) {
+        sm.seg[0] = sm.seg[1] = m0 + mass + tail;
+        sm.seg[2] = m0 + mass;  // the bins'
+      }
       __syncthreads();
       m_all = sm.seg[0];
     }
@@ -915,10 +1046,11 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
     }
     const int last = q.use_k ? q.bk : kBins - 1;
     if (use_p) {
-      // a bin's true mass is between m and m + its tokens (truncated units), to 1e-4
+      // a bin's true mass is between m and m + its tokens (truncated units), well to 1e-4
       const double pp = tp > 0.0f ? (double)tp : 0.0;
       const double w_lo = pp * (double)sm.seg[0] * 0.9998 - (double)p.V,
                    w_hi = pp * ((double)sm.seg[1] + p.V) * 1.0002 + 1.0;
+      if (!q.use_k && turn == 0 && spread > 8.0f * T && (double)sm.seg[2] < w_hi) continue;  // the cut may be in the tail
 #pragma unroll
       for (int e = 0; e < BPT; ++e) {
         const int b = tid * BPT + e;
@@ -942,25 +1074,27 @@ __global__ void __launch_bounds__(NT) sample_kernel(const SampleParams p) {
     __syncthreads();
     q.cnt_above = sm.cnt_b1;
     q.n1 = sm.cnt_b2 - q.cnt_above;
+    const double per1 = 1.0 / (double)(1u << (2 * p.half));
+    q.z_lo = (double)m_all * per1 * (1.0 - Expo32::kHist);
+    q.z_hi = ((double)m_all + p.V) * per1 * (1.0 + Expo32::kHist);
     const int in_bk = q.use_k ? (int)sm.h.cnt[q.bk] : 0;
     q.fits = q.n1 + (q.use_k && q.bk > q.b2 ? in_bk : 0) <= NT;
     __syncthreads();
-    if (!q.use_k && q.cnt_above + q.n1 <= kListMax) {
+    if (!q.use_k && q.cnt_above + q.n1 <= NT && Expo32::usable(mx, T)) {
       // A small nucleus: all its tokens fit the list, and the mass from the
-      // histogram (fp32 weights: off by less than 6e-6 and a unit a token) settles
-      // the cut unless it falls that close to a token's border.
-      const float edge = Cut::kOne + (float)q.b2;
-      walk<STAGED ? 2 : 4>(r, [&](int j, float l) {
-        if (l > -INFINITY && q.fbin(l) <= edge) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l, j);
-      });
-      const double per = exp2((double)(sh - 2 * p.half));
-      const int64_t z_lo = (int64_t)((double)m_all * per * (1.0 - 6e-6)),
-                    z_hi = (int64_t)(((double)m_all + p.V) * per * (1.0 + 6e-6)) + 1;
-      __syncthreads();
+      // histogram (off by less than kHist and a unit a token) settles the cut
+      // unless it falls that close to a token's border.
+      const float edge = Cut::kOne + (float)q.b2;  // (b2 is the last bin: what is past it weighs nothing)
+      collect<NT, 2>(r, sm.own, sm.cand, NT, &sm.ncand,
+                     [&](float l) { return l > -INFINITY && q.fbin(l) <= edge; });
+      const double per = sh >= 2 * p.half ? (double)((int64_t)1 << (sh - 2 * p.half)) : 1.0 / (double)(1 << (2 * p.half - sh));
+      const int64_t z_lo = (int64_t)((double)m_all * per * (1.0 - Expo32::kHist)),
+                    z_hi = (int64_t)(((double)m_all + p.V) * per * (1.0 + Expo32::kHist)) + 1;
       if (pick_from_list<NT>(q.cnt_above + q.n1, INT_MAX, tp, z_lo, z_hi, wmin, u, weight, T, sm, p, row, r.off))
         return;
       __syncthreads();
     }
+    break;
   }
   if (q.fits && u < 1.0f && Expo32::usable(mx, T)) {
     if (pick_from_row<NT, false>(r, q, tp, mp, u, T, weight, sm, p, row)) return;
@@ -989,12 +1123,12 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   const int sh = 62 - bits < 51 ? 62 - bits : 51;
   const int half = 31 - bits < 15 ? 31 - bits : 15;  // V tokens in one bin do not overflow a sum
   const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, half};
-  // Rows for every SM and more: two a SM, one loads while the other computes (from
-  // L2 after its first pass).  Fewer: a row's later passes from shared memory.
-  if (M > device_sm_count()) return launch_t<512, false>(p, M, 0, stream);
+  // Rows for every SM and more: some on each SM, they load and compute in turn (from
+  // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
+  if (M > device_sm_count()) return launch_t<256, false>(p, M, 0, stream);
   const size_t smem = ((size_t)V + 7) / 4 * 16;
-  if (smem <= 160 * 1024) return launch_t<1024, true>(p, M, smem, stream);
-  return launch_t<1024, false>(p, M, 0, stream);
+  if (smem <= 160 * 1024) return launch_t<512, true>(p, M, smem, stream);
+  return launch_t<512, false>(p, M, 0, stream);
 }
 
 }  // namespace nc

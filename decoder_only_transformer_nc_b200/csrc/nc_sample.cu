@@ -70,6 +70,27 @@ __constant__ double kExp2[32] = {
     1.681792830507429, 1.7186192981224779, 1.7562521603732995, 1.7947090750031072,
     1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002};
 
+// fp64 of an fp32 value, on the bits: the conversion instruction runs at a few
+// values a cycle and bounded these passes.  Zero and subnormals come out below
+// 2^-126 in size too, infinities and NaN as something finite.
+__device__ __forceinline__ double wide(float x) {
+  const int u = __float_as_int(x);
+  return __hiloint2double(((u >> 3) & (int)0x8fffffffu) + (896 << 20), u << 29);
+}
+
+// A sum of fp32 values in [0, 1] (a little more for rounding) in two fp32 parts:
+// what an addition rounds off is kept.  It starts at 2, so the sum is never the
+// smaller one, which makes the rounded-off part exact in two operations.
+struct Sum2 {
+  float hi = 2.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = hi + x;
+    lo += x - (t - hi);
+    hi = t;
+  }
+  __device__ __forceinline__ double value() const { return ((double)hi - 2.0) + (double)lo; }
+};
+
 // A row's exponential: exp((l - mx) / T) in units of 2^-sh, rounded to nearest.
 // 2^y, y = (l - mx) log2(e) / T, in fp64: y = (32 n + j) / 32 + f with |f| <=
 // 1/64, 2^f by the Taylor series of e^(f ln 2) to the 5th power (remainder
@@ -90,7 +111,7 @@ struct Expo {
   // The weight as the low bits of 2^52 + weight: sums of these are exact too.
   __device__ __forceinline__ int64_t raw(float l) const {
     const bool counts = l == mx || (l - mx) * c32 > least;
-    const double d = l == mx ? 0.0 : (double)l - mxd;
+    const double d = l == mx ? 0.0 : wide(l) - mxd;
     constexpr double kMagic = 6755399441055744.0 / 32;  // 1.5 2^52 / 32: adding it rounds to 1/32
     const double t = fma(d, c, kMagic);
     const int nj = __double2loint(t);
@@ -110,15 +131,13 @@ struct Expo {
   __device__ __forceinline__ int64_t operator()(float l) const { return raw(l) - kRaw0; }
 };
 
-// The same as an fp32 number (1 for the maximum): y = n + f in two fp32 parts (the
-// difference's and the product's low parts kept), 2^f by the hardware, n into the
-// exponent.
+// The same as an fp32 number (1 for the maximum): y = n + f, the remainder f from
+// the unrounded product, 2^f by the hardware, n into the exponent.
 struct Expo32 {
   float mx, least, c_hi, c_lo;
-  // Relative error of a weight: 2^-22 (2^f), 2^-25 ln 2 (f), and, where |l| > |mx|
-  // makes the difference's low part inexact, 2^-24 |y| ln 2; sums of four add
-  // three times 2^-24.
-  static constexpr double kErr = 5e-7, kErrY = 4.5e-8;
+  // Relative error of a weight: 2^-22 (2^f), 2^-24 ln 2 (f), and 2^-24 |y| ln 2 (the
+  // difference l - mx).
+  static constexpr double kErr = 3e-7, kErrY = 4.5e-8;
   static constexpr double kHist = 2e-6;  // the two for |y| < 31: a sum of weights from 2^-30 on
 
   __device__ Expo32(float mx_, double c, float T) : mx(mx_) {
@@ -129,14 +148,13 @@ struct Expo32 {
   __device__ static bool usable(float mx, float T) {
     return T > 1e-20f && T < 1e20f && fabsf(mx) < 1e5f * T;
   }
-  __device__ __forceinline__ float operator()(float l, float& y) const {
-    const float lc = fmaxf(l, least);  // also -inf and NaN
-    const float d = lc - mx, d_lo = lc - (d + mx);
-    y = d * c_hi;
-    const float y_lo = fmaf(d_lo, c_hi, fmaf(d, c_lo, fmaf(d, c_hi, -y)));
-    const float t = y + 12582912.0f;  // 1.5 2^23: the nearest integer in the low bits
+  // d: l - mx
+  __device__ __forceinline__ float operator()(float l, float& d) const {
+    d = fmaxf(l, least) - mx;  // also -inf and NaN
+    constexpr float kMagic = 12582912.0f;  // 1.5 2^23: the nearest integer in the low bits
+    const float t = fmaf(d, c_hi, kMagic);
     float w;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((y - (t - 12582912.0f)) + y_lo));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(d, c_lo, fmaf(d, c_hi, kMagic - t))));
     return __int_as_float(__float_as_int(w) + (__float_as_int(t) << 23));
   }
 };
@@ -165,15 +183,27 @@ __device__ __forceinline__ float4 load4(const Row& r, int j) {
 // at a time; positions outside the row come as NaN.  U loads are in flight.
 template <int U, typename F>
 __device__ __forceinline__ void walk4(const Row& r, F f) {
+  int j0 = r.seg0 + (threadIdx.x & 31) * 4;
+  if constexpr (U == 1) {  // long f: one copy of its code, the next load on its way
+    float4 v;
+    if (j0 < r.seg1) v = load4(r, j0);
 #pragma unroll 1
-  for (int j0 = r.seg0 + (threadIdx.x & 31) * 4; j0 < r.seg1; j0 += 128 * U) {
-    float4 v[U];
+    for (; j0 < r.seg1; j0 += 128) {
+      const float4 w = v;
+      if (j0 + 128 < r.seg1) v = load4(r, j0 + 128);
+      f(j0, w);
+    }
+  } else {
+#pragma unroll 1
+    for (; j0 < r.seg1; j0 += 128 * U) {
+      float4 v[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (j0 + k * 128 < r.seg1) v[k] = load4(r, j0 + k * 128);
+      for (int k = 0; k < U; ++k)
+        if (j0 + k * 128 < r.seg1) v[k] = load4(r, j0 + k * 128);
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (j0 + k * 128 < r.seg1) f(j0 + k * 128, v[k]);
+      for (int k = 0; k < U; ++k)
+        if (j0 + k * 128 < r.seg1) f(j0 + k * 128, v[k]);
+    }
   }
 }
 
@@ -519,7 +549,6 @@ struct Cut {
   static constexpr float kOne = 8388608.0f;  // 2^23: the sum's last bit is 1
   static constexpr float kFar = kOne + (float)(kBins - 1);
   __device__ __forceinline__ float fbin(float l) const { return fmaf(mx - l, scale, kOne); }
-  __device__ __forceinline__ int bin(float l) const { return __float_as_int(fminf(fbin(l), kFar)) - 0x4b000000; }
 };
 
 // The row's token from its bracket: a pass that sums every segment's sure tokens
@@ -548,12 +577,6 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
       return (A)wf(l, y);
     }
   };
-  // small weights are added in fp32 first; beside a large one they would lose their
-  // last bits, which the logprob of a likely token shows
-  auto sum4 = [](float a, float b, float c, float d) -> double {
-    if (fmaxf(fmaxf(a, b), fmaxf(c, d)) > 0.004f) return ((double)a + (double)b) + ((double)c + (double)d);
-    return (double)((a + b) + (c + d));
-  };
   // a bin as a bound of fbin: with top-k the last one took in all beyond it
   auto upto = [&](int b) { return q.use_k && b >= kBins - 1 ? INFINITY : Cut::kOne + (float)b; };
   const float f1 = Cut::kOne + (float)q.b1, f2 = upto(q.b2), fk = Cut::kOne + (float)q.bk, fk2 = upto(q.bk);
@@ -565,6 +588,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   bool good = q.fits;
   A za = 0, zt = 0, mass = 0;  // before the bracket; all that top-p's share is of; kept of the segment
   double e1 = 0.0;             // sum of w |y|
+  Sum2 as, ts, ms;
   if (good) {
     if constexpr (EXACT) {
       uint64_t sum = 0;  // modulo 2^64 until the 2^52 of every position is taken off
@@ -595,7 +619,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
         if (q.bins && !use_m) mass = za;
       }
     } else if (!q.bins) {
-      walk4<4>(r, [&](int, const float4& v) {
+      walk4<1>(r, [&](int, const float4& v) {
         float y0, y1, y2, y3;
         float w0 = wf(v.x, y0), w1 = wf(v.y, y1), w2 = wf(v.z, y2), w3 = wf(v.w, y3);
         s1 = fmaf(w0, y0, fmaf(w1, y1, fmaf(w2, y2, fmaf(w3, y3, s1))));
@@ -608,13 +632,16 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
           w2 = w2 >= m ? w2 : 0.0f;
           w3 = w3 >= m ? w3 : 0.0f;
         }
-        mass += sum4(w0, w1, w2, w3);
+        ms.add(w0);
+        ms.add(w1);
+        ms.add(w2);
+        ms.add(w3);
       });
     } else {
       // tokens past the bracket (with top-k: past its bin) need no weight: without
       // top-k, top-p's mass comes from the histogram
       const float fl = q.use_k ? fk2 : f2;
-      walk4<2>(r, [&](int j, const float4& v) {
+      walk4<1>(r, [&](int j, const float4& v) {
         const float l[4] = {v.x, v.y, v.z, v.w};
         const float b[4] = {q.fbin(v.x), q.fbin(v.y), q.fbin(v.z), q.fbin(v.w)};
         if (!(fminf(fminf(b[0], b[1]), fminf(b[2], b[3])) <= fl)) return;  // NaN gives way to the others
@@ -628,22 +655,25 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
           t[e] = b[e] > f2 && b[e] < fk ? w : 0.0f;
           if (!(b[e] < f1) && listed(l[e], b[e])) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l[e], j + e);
         }
-        const double a4 = sum4(a[0], a[1], a[2], a[3]);
-        za += a4;
-        zt += a4;
-        if (q.use_k) zt += sum4(t[0], t[1], t[2], t[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) as.add(a[e]);
+        if (q.use_k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ts.add(t[e]);
         if (use_m) {
           const float m = (float)wmin;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             open = open || fabsf(a[e] - m) <= m * 1e-5f;
-            a[e] = a[e] >= m ? a[e] : 0.0f;
+            ms.add(a[e] >= m ? a[e] : 0.0f);
           }
-          mass += sum4(a[0], a[1], a[2], a[3]);
-        } else {
-          mass += a4;
         }
       });
+    }
+    if constexpr (!EXACT) {
+      za = as.value();
+      zt = za + ts.value();
+      mass = q.bins && !use_m ? za : ms.value();
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
@@ -668,7 +698,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     z_all = zt + (nc > 0 ? cums[nc - 1] : A(0));
     double err = 0.0;
     if constexpr (!EXACT) {
-      e1 = block_reduce<NT>((double)s1, sm.red, Add{}, 0.0);
+      e1 = block_reduce<NT>((double)s1 * (double)wf.c_hi, sm.red, Add{}, 0.0);
       err = 2.0 * (Expo32::kErr * z_all - Expo32::kErrY * e1);
     }
     if (q.use_p) {
@@ -735,7 +765,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   }
   if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = mass;
   if constexpr (!EXACT) {
-    if (!q.bins) e1 = block_reduce<NT>((double)s1, sm.red, Add{}, 0.0);
+    if (!q.bins) e1 = block_reduce<NT>((double)s1 * (double)wf.c_hi, sm.red, Add{}, 0.0);
     if (use_m && __syncthreads_or(open)) return false;
   }
   __syncthreads();
@@ -989,18 +1019,27 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     const Expo32 wf(mx, sm.c, T);
     const float unit = (float)(1u << (2 * p.half));
     int64_t tail = 0;
-    walk<1>(r, [&](int, float l) {
-      if (!(l > -INFINITY)) return;
-      float y;
-      const uint32_t m = !use_p ? 0u : l == mx ? 1u << (2 * p.half) : (uint32_t)(wf(l, y) * unit);
-      if (!q.use_k && q.fbin(l) > Cut::kFar) {
-        tail += m;
-      } else {
-        const int b = q.bin(l);
-        atomicAdd(&sm.h.cnt[b], 1u);
-        if (m) {
-          atomicAdd(&sm.h.lo[b], m & ((1u << p.half) - 1u));
-          if (m >> p.half) atomicAdd(&sm.h.hi[b], m >> p.half);
+    walk4<1>(r, [&](int, const float4& v) {
+      const float l[4] = {v.x, v.y, v.z, v.w};
+      uint32_t m[4];
+      float b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y;
+        m[e] = use_p ? (uint32_t)(wf(l[e], y) * unit) : 0u;  // 0 for -inf and NaN
+        b[e] = q.fbin(l[e]);
+      }
+      // (-inf and NaN fall out of every bin; with top-k only NaN and -inf beyond a bin's reach do)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!q.use_k) tail += b[e] <= Cut::kFar ? 0u : m[e];
+        if (q.use_k ? l[e] > -INFINITY : b[e] <= Cut::kFar) {
+          const int at = __float_as_int(fminf(b[e], Cut::kFar)) - 0x4b000000;
+          atomicAdd(&sm.h.cnt[at], 1u);
+          if (m[e]) {
+            atomicAdd(&sm.h.lo[at], m[e] & ((1u << p.half) - 1u));
+            if (m[e] >> p.half) atomicAdd(&sm.h.hi[at], m[e] >> p.half);
+          }
         }
       }
     });

@@ -402,7 +402,8 @@ class Session:
         token.  ``accept_tree`` then moves the path that the samples confirm
         into the cache; without it the tree is dropped."""
         import torch
-        cfg, dev = self.model.cfg, self.buffer.device
+        cfg, device = self.model.cfg, self.buffer.device
+        dev = self.buffer.get_device()
         where = "Session.decode_tree"
         if tokens.dim() != 2 or tokens.shape[0] != self.B:
             raise NcError(3, f"{where}: tokens {tuple(tokens.shape)}, rows {self.B}")
@@ -415,9 +416,9 @@ class Session:
         with _allocate_on(stream):
             lens = self.lens
             if self._tree_ws is None or self._tree_ws.numel() < need:
-                self._tree_ws = torch.empty(need, dtype=torch.uint8, device=dev)
+                self._tree_ws = torch.empty(need, dtype=torch.uint8, device=device)
             if logits is None:
-                logits = torch.empty((self.B, N, cfg.vocab), dtype=torch.float32, device=dev)
+                logits = torch.empty((self.B, N, cfg.vocab), dtype=torch.float32, device=device)
         lp = _arg(where, "logits", logits, torch.float32, (self.B, N, cfg.vocab), dev)
         self._tree = None
         _launch(where, dev, stream, lib().nc_decode_tree, ctypes.byref(cfg), ctypes.byref(self.model.weights), tp, pp,
@@ -437,11 +438,11 @@ class Session:
         if self._tree is None:
             raise NcError(1, f"{where}: no decode_tree before it")
         tokens, parents, lens = self._tree
-        dev, N = self.buffer.device, tokens.shape[1]
+        device, dev, N = self.buffer.device, self.buffer.get_device(), tokens.shape[1]
         sp = _arg(where, "sampled", sampled, torch.int32, (self.B, N), dev)
         with _allocate_on(stream):
-            path = torch.empty((self.B, N), dtype=torch.int32, device=dev)
-            count, nxt, lens_out = (torch.empty(self.B, dtype=torch.int32, device=dev) for _ in range(3))
+            path = torch.empty((self.B, N), dtype=torch.int32, device=device)
+            count, nxt, lens_out = (torch.empty(self.B, dtype=torch.int32, device=device) for _ in range(3))
         _launch(where, dev, stream, lib().nc_accept_tree, ctypes.byref(self.model.cfg), tokens.data_ptr(),
                 parents.data_ptr(), sp, lens.data_ptr(), self.B, N, path.data_ptr(), count.data_ptr(), nxt.data_ptr(),
                 lens_out.data_ptr(), self.buffer.data_ptr(), self.buffer.numel(), self.T_max,
@@ -736,35 +737,39 @@ def loss_mean(token_loss, targets, V, loss, stream=None):
 # ---------------------------------------------------------------- drafted trees, sampling, distillation
 
 def _arg(where, name, t, dtype, shape, dev):
-    """Checks one tensor argument; returns its address (0 for an absent one)."""
+    """Checks one tensor argument (dev: its device's index, -1 for the host);
+    returns its address (0 for an absent one)."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise NcError(3, f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise NcError(1, f"{where}: {name} is not contiguous")
-    if t.device != dev:
-        raise NcError(1, f"{where}: {name} is on {t.device}, expected {dev}")
-    return t.data_ptr()
+    raise NcError(1, f"{where}: {name} is on {t.device}, the first tensor is on another device")
 
 
 def _launch(where, dev, stream, fn, *args):
-    """Calls a library function on the tensors' device, on ``stream`` (of that
-    device) or its current stream."""
+    """Calls a library function on device ``dev`` (an index), on ``stream`` (of
+    that device) or the device's current stream."""
     import torch
-    if dev.type != "cuda":
-        raise NcError(8, f"{where}: tensors are on {dev}")
+    if dev < 0:
+        raise NcError(8, f"{where}: the tensors are not on a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise NcError(1, f"{where}: the stream is on {stream.device}, the tensors are on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        code = fn(*args, stream.cuda_stream)
+        # the public torch.cuda.current_stream builds a Stream object: 2 us, half a launch
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise NcError(1, f"{where}: the stream is on {stream.device}, the tensors are on cuda:{dev}")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, stream.cuda_stream)
+            code = fn(*args, raw)
     if code != 0:
         raise NcError(code, where)
 
@@ -787,7 +792,7 @@ def tree_mask(parents, mask, stream=None):
     if parents.dim() != 2:
         raise NcError(3, f"{where}: parents {tuple(parents.shape)}")
     B, N = parents.shape
-    dev = parents.device
+    dev = parents.get_device()
     a = (_arg(where, "parents", parents, torch.int32, (B, N), dev),
          _arg(where, "mask", mask, torch.int32, (B, N, (N + 31) // 32), dev))
     _launch(where, dev, stream, lib().nc_tree_mask, *a, B, N)
@@ -807,7 +812,7 @@ def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stre
         raise NcError(3, f"{where}: q {tuple(q.shape)}, cache {tuple(cache.shape)}")
     B, N, H, D = q.shape
     T_max, Hkv = cache.shape[1], cache.shape[3]
-    dev, dt = q.device, q.dtype
+    dev, dt = q.get_device(), q.dtype
     qs = H * D
     if not q.is_contiguous():  # e.g. the q columns of a packed q | k | v
         qs = q.stride(1) if N > 1 else (q.stride(0) if B > 1 else qs)
@@ -820,12 +825,13 @@ def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stre
     if B == 0:
         return
     need = lib().nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, window)
-    if workspace is None and need and dev.type == "cuda":
+    wp = wn = 0
+    if workspace is None and need and dev >= 0:
         with _allocate_on(stream):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if workspace is not None and workspace.device != dev:
-        raise NcError(1, f"{where}: the workspace is on {workspace.device}, expected {dev}")
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        wn = workspace.numel()
+        wp = _arg(where, "workspace", workspace, torch.uint8, (wn,), dev)
     _launch(where, dev, stream, lib().nc_tree_attention, q.data_ptr(), qs, *a, B, N, H, Hkv, D, T_max, window, _dt(q),
             wp, wn)
 
@@ -844,7 +850,7 @@ def sample(logits, u, tokens, logprob=None, temperature=None, top_k=None, top_p=
     ld = logits.stride(0) if M > 1 else V
     if V > 1 and logits.stride(1) != 1 or ld < V:
         raise NcError(1, f"{where}: logits strides {logits.stride()}: only the rows may be strided")
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
     if u is None or tokens is None:
         raise NcError(1, f"{where}: u and tokens are needed")
     a = (_arg(where, "u", u, f32, (M,), dev), _arg(where, "temperature", temperature, f32, (M,), dev),
@@ -869,7 +875,7 @@ def tree_accept(tokens, parents, mask, sampled, lens, kv, cache, path, count, ne
     L, B, N, _, Hkv, D = kv.shape
     T_max = cache.shape[2]
     _dt(kv)
-    dev, i32, bn, b1 = kv.device, torch.int32, (B, N), (B,)
+    dev, i32, bn, b1 = kv.get_device(), torch.int32, (B, N), (B,)
     a = (_arg(where, "tokens", tokens, i32, bn, dev), _arg(where, "parents", parents, i32, bn, dev),
          _arg(where, "mask", mask, i32, (B, N, (N + 31) // 32), dev), _arg(where, "sampled", sampled, i32, bn, dev),
          _arg(where, "lens", lens, i32, b1, dev), _arg(where, "kv", kv, kv.dtype, (L, B, N, 2, Hkv, D), dev),
@@ -894,7 +900,7 @@ def distill_topk(z, teacher_idx, teacher_logits, token_loss, dz=None, tau=1.0, c
         raise NcError(3, f"{where}: z {tuple(z.shape)}, teacher_idx {tuple(teacher_idx.shape)}")
     M, V = z.shape
     K = teacher_idx.shape[1]
-    dev, f32 = z.device, torch.float32
+    dev, f32 = z.get_device(), torch.float32
     if token_loss is None or teacher_logits is None:
         raise NcError(1, f"{where}: teacher_logits and token_loss are needed")
     a = (_arg(where, "z", z, f32, (M, V), dev), _arg(where, "teacher_idx", teacher_idx, torch.int32, (M, K), dev),
@@ -907,4 +913,4 @@ def distill_topk(z, teacher_idx, teacher_logits, token_loss, dz=None, tau=1.0, c
         dzp = _arg(where, "dz", dz, dz.dtype, (M, V), dev)
     if M:
         _launch(where, dev, stream, lib().nc_distill_topk, *a, dzp, kind, M, V, K, tau, cap,
-                None if status is None else status.data_ptr())
+                _arg(where, "status", status, None if status is None else status.dtype, None if status is None else status.shape, dev))

@@ -278,6 +278,7 @@ __device__ __forceinline__ uint64_t code_of(float l, int pos) {
   return ((uint64_t)key_of(l) << 32) | (uint32_t)~pos;
 }
 
+constexpr int kStageBytes = 160 * 1024;  // rows up to this are staged in shared memory
 constexpr int kTopBins = 256;  // histogram of the threads' maxima
 
 template <int NT>
@@ -1145,8 +1146,16 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
 template <int NT, bool STAGED>
 nc_status launch_t(const SampleParams& p, int M, size_t smem, cudaStream_t stream) {
   auto* fn = sample_kernel<NT, STAGED>;
-  if (smem > 0 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return NC_ERR_CUDA;
+  if (smem > 0) {
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_done[dev]) {
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes) != cudaSuccess)
+        return NC_ERR_CUDA;
+      if (dev < 64) attr_done[dev] = true;
+    }
+  }
   fn<<<M, NT, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
 }
@@ -1166,7 +1175,7 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
   if (M > device_sm_count()) return launch_t<256, false>(p, M, 0, stream);
   const size_t smem = ((size_t)V + 7) / 4 * 16;
-  if (smem <= 160 * 1024) return launch_t<512, true>(p, M, smem, stream);
+  if (smem <= kStageBytes) return launch_t<512, true>(p, M, smem, stream);
   return launch_t<512, false>(p, M, 0, stream);
 }
 

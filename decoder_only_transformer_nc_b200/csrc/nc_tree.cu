@@ -337,7 +337,13 @@ nc_status tree_attn_run(const TreeAttnParams& p, int B, cudaStream_t stream) {
   constexpr int smem = kStages * 2 * kTK * (D + 8) * 2;
   static_assert(smem >= 4 / RW * ROWS * (D + 4 + 2) * 4, "the partial results reuse the stages");
   auto* fn = tree_attn_kernel<D, F16, RW>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return NC_ERR_CUDA;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_done[dev]) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return NC_ERR_CUDA;
+    if (dev < 64) attr_done[dev] = true;
+  }
   const int G = p.H / p.Hkv;
   const int row_tiles = (p.N * G + ROWS - 1) / ROWS;
   const int base = row_tiles * p.Hkv * B;

@@ -46,17 +46,6 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-template <bool MAX>
-__device__ __forceinline__ float block_all(float v, float* red) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  v = MAX ? warp_max(v) : warp_sum(v);
-  __syncthreads();
-  if (lane == 0) red[w] = v;
-  __syncthreads();
-  float t = lane < kThreads / 32 ? red[lane] : (MAX ? -INFINITY : 0.0f);
-  return MAX ? warp_max(t) : warp_sum(t);
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -69,35 +58,34 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// tanh(u).  Up to |u| = 0.55, where most logits are under their cap, the odd
-// series u - u^3/3 + 2 u^5/15 - ... to u^13 (the next term is 8e-7 of u there):
-// no special-function unit, which would bound these passes.  Beyond, 1 - 2 /
-// (e^2u + 1), whose absolute error is that of its 1.
-__device__ __forceinline__ float tanh_small(float u) {
+// tanh(u).  Up to |u| = 1.5, where nearly all logits are under their cap, the
+// continued fraction u / (1 + s / (3 + s / (5 + s / (7 + s / (9 + s / 11))))),
+// s = u^2, as a quotient of polynomials: within 3e-8 there, one reciprocal.
+// Beyond, 1 - 2 / (e^2u + 1), whose absolute error is that of its 1.
+constexpr float kNear = 1.5f;
+__device__ __forceinline__ float tanh_near(float u) {
   const float s = u * u;
-  float r = 3.5921280365724810e-03f;               // 21844 / 6081075
-  r = fmaf(r, s, -8.8632355299021966e-03f);        // -1382 / 155925
-  r = fmaf(r, s, 2.1869488536155203e-02f);         // 62 / 2835
-  r = fmaf(r, s, -5.3968253968253971e-02f);        // -17 / 315
-  r = fmaf(r, s, 1.3333333333333333e-01f);         // 2 / 15
-  r = fmaf(r, s, -3.3333333333333331e-01f);        // -1 / 3
-  return fmaf(r * s, u, u);
+  const float a = fmaf(fmaf(21.0f / 10395.0f, s, 1260.0f / 10395.0f), s, 1.0f);
+  const float b = fmaf(fmaf(fmaf(1.0f / 10395.0f, s, 210.0f / 10395.0f), s, 4725.0f / 10395.0f), s, 1.0f);
+  return u * a * rcp(b);
 }
-__device__ __forceinline__ float tanh_any(float u) {
+__device__ __forceinline__ float tanh_far(float u) {
   return copysignf(fmaf(-2.0f, rcp(1.0f + ex2(2.0f * kLog2e * fabsf(u))), 1.0f), u);
 }
+__device__ __forceinline__ float tanh_of(float u) { return fabsf(u) <= kNear ? tanh_near(u) : tanh_far(u); }
 
-// The four logits' tanh; the slow form only where some lane of the warp needs it.
-__device__ __forceinline__ void tanh4(const float4& z, float inv_cap, float (&t)[4]) {
-  const float u[4] = {z.x * inv_cap, z.y * inv_cap, z.z * inv_cap, z.w * inv_cap};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) t[e] = tanh_small(u[e]);
-  const float m = fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])));
-  if (!(m <= 0.55f)) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (!(fabsf(u[e]) <= 0.55f)) t[e] = tanh_any(u[e]);
+// The tanh of four logits; the far form only where some lane of the warp needs it.
+__device__ __forceinline__ float4 tanh4(const float4& z, float inv_cap) {
+  const float4 u = make_float4(z.x * inv_cap, z.y * inv_cap, z.z * inv_cap, z.w * inv_cap);
+  float4 t = make_float4(tanh_near(u.x), tanh_near(u.y), tanh_near(u.z), tanh_near(u.w));
+  const float m = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w)));
+  if (!(m <= kNear)) {
+    if (!(fabsf(u.x) <= kNear)) t.x = tanh_far(u.x);
+    if (!(fabsf(u.y) <= kNear)) t.y = tanh_far(u.y);
+    if (!(fabsf(u.z) <= kNear)) t.z = tanh_far(u.z);
+    if (!(fabsf(u.w) <= kNear)) t.w = tanh_far(u.w);
   }
+  return t;
 }
 
 // (maximum, sum) of two parts of a softmax, log2 domain.
@@ -113,19 +101,25 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 // 256 threads share an SM, at different points of different rows: one loads
 // while another computes or stores.  The threads' (maximum, sum) are joined over
 // the block and, through distributed shared memory, over the cluster, in a fixed
-// order.  REGS = 0: longer rows, one CTA, read again from L2 for each use.
+// order.  The teacher's entries are one warp's business: with K = 64 beside 8192
+// logits, eight warps repeating it took as many instructions as the row.
+// REGS = 0: longer rows, one CTA, read again from L2 for each use.
 // Groups of four start at 16-byte boundaries of z's row (the ends and a dz that is
 // not aligned alike go by single elements).
 // DZ: 0 none, 1 fp32, 2 bf16, 3 fp16
 template <int DZ, bool CAP, int REGS>
-__global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1) distill_kernel(const DistillParams p, int slice) {
-  extern __shared__ float q_s[];  // [K] probabilities, then [K] indices
-  __shared__ float red[32];
+__global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
+    distill_kernel(const DistillParams p, int slice, int slots) {
+  extern __shared__ float q_s[];  // [K] logits, then probabilities; [K] z of the entry; [K] indices; [slots]
   __shared__ float2 part[8], part_w[kThreads / 32];
-  int32_t* i_s = reinterpret_cast<int32_t*>(q_s + p.K);
+  __shared__ float tlse_s;
+  __shared__ int any_s, twice_s;
+  float* z_s = q_s + p.K;
+  int32_t* i_s = reinterpret_cast<int32_t*>(z_s + p.K);
+  int32_t* table = i_s + p.K;
   const int64_t row = blockIdx.y;
   const int rank = blockIdx.x, CS = gridDim.x;  // the cluster spans the grid's x
-  const int V = p.V, K = p.K, tid = threadIdx.x;
+  const int V = p.V, K = p.K, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* zr = p.z + row * V;
   const int off = (int)((reinterpret_cast<uintptr_t>(zr) >> 2) & 3);  // logit 0 is position off
   const float* z = zr - off;
@@ -146,17 +140,18 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1) distill_kernel(co
   };
   constexpr int STEP = kThreads * 4;
   const int j_first = s0 + tid * 4;
+  const int nr = (s1 - j_first + STEP - 1) / STEP;  // groups of this thread (0 or less: none)
   float4 keep[REGS > 0 ? REGS : 1];
   if constexpr (REGS > 0) {
 #pragma unroll
     for (int r = 0; r < REGS; ++r)
-      if (j_first + r * STEP < s1) keep[r] = load(j_first + r * STEP);
+      if (r < nr) keep[r] = load(j_first + r * STEP);
   }
   auto each = [&](auto f) {
     if constexpr (REGS > 0) {
 #pragma unroll
       for (int r = 0; r < REGS; ++r)
-        if (j_first + r * STEP < s1) f(j_first + r * STEP, keep[r]);
+        if (r < nr) f(j_first + r * STEP, keep[r]);
     } else {
 #pragma unroll 1
       for (int j = j_first; j < s1; j += STEP) {
@@ -166,64 +161,87 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1) distill_kernel(co
     }
   };
 
-  // teacher's softmax (every CTA for itself), while the row is on its way
-  float tm = -INFINITY;
-  for (int k = tid; k < K; k += kThreads) {
-    int i = p.idx[row * K + k];
-    if (i < -1 || i >= V) {
-      if (p.status) atomicOr(p.status, NC_DEV_TARGET_RANGE);
-      i = -1;
+  // the teacher's softmax, while the row is on its way
+  if (warp == 0) {
+    float tm = -INFINITY;
+    for (int k = lane; k < slots; k += 32) table[k] = -1;
+    for (int k = lane; k < K; k += 32) {
+      int i = p.idx[row * K + k];
+      if (i < -1 || i >= V) {
+        if (p.status) atomicOr(p.status, NC_DEV_TARGET_RANGE);
+        i = -1;
+      }
+      const float t = i < 0 ? -INFINITY : p.teacher[row * K + k] * inv_tau;
+      z_s[k] = i < 0 ? 0.0f : zr[i];
+      i_s[k] = i;
+      q_s[k] = t;
+      tm = fmaxf(tm, t);
     }
-    const float t = i < 0 ? -INFINITY : p.teacher[row * K + k] * inv_tau;
-    i_s[k] = i;
-    q_s[k] = t;
-    tm = fmaxf(tm, t);
+    tm = warp_max(tm);
+    const bool any = tm != -INFINITY;
+    float ts = 0.0f;
+    for (int k = lane; k < K; k += 32) ts += any ? expf(q_s[k] - tm) : 0.0f;
+    ts = warp_sum(ts);
+    bool twice = false;
+    if (DZ != 0) {  // is an index given more than once?  (a table of 2 K slots or more)
+      __syncwarp();
+      for (int k = lane; k < K; k += 32) {
+        const int i = i_s[k];
+        for (int h = i; i >= 0; ++h) {
+          const int was = atomicCAS(&table[h & (slots - 1)], -1, i);
+          twice = twice || was == i;
+          if (was == -1 || was == i) break;
+        }
+      }
+      twice = __any_sync(0xffffffffu, twice);
+    }
+    if (lane == 0) {
+      any_s = any;
+      twice_s = twice;
+      tlse_s = any ? tm + logf(ts) : 0.0f;
+    }
   }
-  tm = block_all<true>(tm, red);
-  const bool any = tm != -INFINITY;
-  float ts = 0.0f;
-  for (int k = tid; k < K; k += kThreads) ts += any ? expf(q_s[k] - tm) : 0.0f;
-  ts = block_all<false>(ts, red);
-  const float tlse = any ? tm + logf(ts) : 0.0f;
 
   // the student's softmax: with registers, t takes the place of z
   float2 ms = make_float2(-INFINITY, 0.0f);
+  auto sum4 = [&](const float4& v, float m) {
+    return (ex2(fmaf(v.x, kx, -m)) + ex2(fmaf(v.y, kx, -m))) + (ex2(fmaf(v.z, kx, -m)) + ex2(fmaf(v.w, kx, -m)));
+  };
   each([&](int j, float4& v) {
     if (CAP) {
-      float t[4];
-      tanh4(v, inv_cap, t);
+      v = tanh4(v, inv_cap);
       if (j < off || j + 4 > end) {  // positions outside the row stay -inf
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (j + q < off || j + q >= end) t[q] = -INFINITY;
+        if (j < off || j >= end) v.x = -INFINITY;
+        if (j + 1 < off || j + 1 >= end) v.y = -INFINITY;
+        if (j + 2 < off || j + 2 >= end) v.z = -INFINITY;
+        if (j + 3 < off || j + 3 >= end) v.w = -INFINITY;
       }
-      v = make_float4(t[0], t[1], t[2], t[3]);
     }
+    const float m = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
     if (REGS > 0) {
-      ms.x = fmaxf(ms.x, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+      ms.x = fmaxf(ms.x, m);
     } else {
-      const float m = fmaxf(ms.x, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * kx);
-      if (m != -INFINITY)
-        ms = make_float2(m, ms.y * ex2(ms.x - m) + ((ex2(fmaf(v.x, kx, -m)) + ex2(fmaf(v.y, kx, -m))) +
-                                                    (ex2(fmaf(v.z, kx, -m)) + ex2(fmaf(v.w, kx, -m)))));
+      const float mn = fmaxf(ms.x, m * kx);
+      if (mn != -INFINITY) ms = make_float2(mn, ms.y * ex2(ms.x - mn) + sum4(v, mn));
     }
   });
   if constexpr (REGS > 0) {
     ms.x *= kx;
-    if (ms.x != -INFINITY)
-      each([&](int, float4& v) {
-        ms.y += (ex2(fmaf(v.x, kx, -ms.x)) + ex2(fmaf(v.y, kx, -ms.x))) +
-                (ex2(fmaf(v.z, kx, -ms.x)) + ex2(fmaf(v.w, kx, -ms.x)));
-      });
+    if (ms.x != -INFINITY) each([&](int, float4& v) { ms.y += sum4(v, ms.x); });
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     ms = join(ms, make_float2(__shfl_xor_sync(0xffffffffu, ms.x, o), __shfl_xor_sync(0xffffffffu, ms.y, o)));
-  if ((tid & 31) == 0) part_w[tid >> 5] = ms;
+  if (lane == 0) part_w[warp] = ms;
   __syncthreads();
-  ms = part_w[0];
+  auto join_lanes = [&](const float2* v, int n) {  // n <= 8 parts, in a fixed tree
+    float2 x = lane < n ? v[lane] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) ms = join(ms, part_w[w]);
+    for (int o = 4; o > 0; o >>= 1)
+      x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
+    return make_float2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0));
+  };
+  ms = join_lanes(part_w, kThreads / 32);
   if (CS > 1) {
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
     if (tid < CS)
@@ -231,36 +249,14 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1) distill_kernel(co
                    "f"(ms.x), "f"(ms.y)
                    : "memory");
     cluster_sync();
-    ms = part[0];
-    for (int c = 1; c < CS; ++c) ms = join(ms, part[c]);
+    ms = join_lanes(part, CS);
   }
-  const float xm = ms.x, xs = ms.y, xlse = logf(xs);
+  const float xm = ms.x, xs = ms.y;
+  const bool any = any_s != 0;
 
-  // x of one logit read again (the teacher's entries)
-  auto one = [&](float v, float& t) -> float {
-    const float u = v * inv_cap;
-    t = CAP ? (fabsf(u) <= 0.55f ? tanh_small(u) : tanh_any(u)) : v;
-    return fmaf(t, kx, -xm);
-  };
-  float loss = 0.0f;
-  for (int k = tid; k < K; k += kThreads) {
-    const int i = i_s[k];
-    const float lq = q_s[k] - tlse, q = any ? expf(lq) : 0.0f;
-    if (rank == 0 && q > 0.0f) {
-      float t;
-      loss = fmaf(q, lq - (one(zr[i], t) * 0.6931471805599453f - xlse), loss);
-    }
-    q_s[k] = q;
-  }
-  if (rank == 0) {
-    loss = block_all<false>(loss, red);
-    if (tid == 0) p.loss[row] = any ? p.tau * p.tau * loss : 0.0f;
-  }
-
+  auto slope = [&](float t) { return CAP ? fmaf(-t, t, 1.0f) : 1.0f; };
   if constexpr (DZ != 0) {
-    const float w = any ? p.tau * (p.weight ? p.weight[row] : 1.0f) : 0.0f;
-    const float inv = any ? 1.0f / xs : 0.0f;
-    const float wp = w * inv;
+    const float wp = any ? p.tau * (p.weight ? p.weight[row] : 1.0f) / xs : 0.0f;
     constexpr int ES = DZ == 1 ? 4 : 2;
     uint8_t* dr = static_cast<uint8_t*>(p.dz) + row * V * ES - (int64_t)off * ES;  // position 0
     const bool vec = (reinterpret_cast<uintptr_t>(dr) & (4 * ES - 1)) == 0;
@@ -270,40 +266,61 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1) distill_kernel(co
       else
         reinterpret_cast<uint16_t*>(dr)[j] = (uint16_t)Half<DZ == 3>::pack2(v, 0.0f);
     };
-    auto slope = [&](float t) { return CAP ? fmaf(-t, t, 1.0f) : 1.0f; };
-    each([&](int j, float4& v) {
-      float t[4] = {v.x, v.y, v.z, v.w};
-      if (CAP && REGS == 0) tanh4(v, inv_cap, t);
-      float d[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) d[q] = any ? ex2(fmaf(t[q], kx, -xm)) * wp * slope(t[q]) : 0.0f;
-      if (vec && j >= off && j + 4 <= end) {
-        if constexpr (DZ == 1)
-          __stcs(reinterpret_cast<float4*>(dr + (int64_t)j * 4), make_float4(d[0], d[1], d[2], d[3]));
-        else
-          __stcs(reinterpret_cast<uint2*>(dr + (int64_t)j * 2),
-                 make_uint2(Half<DZ == 3>::pack2(d[0], d[1]), Half<DZ == 3>::pack2(d[2], d[3])));
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (j + q >= off && j + q < end) store1(j + q, d[q]);
-      }
-    });
-    __syncthreads();
-    for (int k = tid; k < K; k += kThreads) {
-      const int i = i_s[k];
-      if (i < 0 || off + i < s0 || off + i >= s1) continue;
-      float q = 0.0f;  // an index given more than once: its first entry stores for all
-      bool first = true;
-      for (int j = 0; j < K; ++j)
-        if (i_s[j] == i) {
-          first = first && j >= k;
-          q += q_s[j];
+    if (any) {
+      each([&](int j, float4& v) {
+        const float4 t = CAP && REGS == 0 ? tanh4(v, inv_cap) : v;
+        const float4 d = make_float4(ex2(fmaf(t.x, kx, -xm)) * (wp * slope(t.x)), ex2(fmaf(t.y, kx, -xm)) * (wp * slope(t.y)),
+                                     ex2(fmaf(t.z, kx, -xm)) * (wp * slope(t.z)), ex2(fmaf(t.w, kx, -xm)) * (wp * slope(t.w)));
+        if (vec && j >= off && j + 4 <= end) {
+          if constexpr (DZ == 1)
+            __stcs(reinterpret_cast<float4*>(dr + (int64_t)j * 4), d);
+          else
+            __stcs(reinterpret_cast<uint2*>(dr + (int64_t)j * 2),
+                   make_uint2(Half<DZ == 3>::pack2(d.x, d.y), Half<DZ == 3>::pack2(d.z, d.w)));
+        } else {
+          if (j >= off && j < end) store1(j, d.x);
+          if (j + 1 >= off && j + 1 < end) store1(j + 1, d.y);
+          if (j + 2 >= off && j + 2 < end) store1(j + 2, d.z);
+          if (j + 3 >= off && j + 3 < end) store1(j + 3, d.w);
         }
-      float t;
-      const float x = one(zr[i], t);
-      if (first) store1(off + i, any ? (ex2(x) * inv - q) * w * slope(t) : 0.0f);
+      });
+    } else {
+      for (int j = max(s0, off) + tid; j < s1; j += kThreads) store1(j, 0.0f);
     }
+    __syncthreads();
+    if (warp == 0 && any) {  // the teacher's entries of this CTA's positions, over what was stored
+      const float tlse = tlse_s, w = p.tau * (p.weight ? p.weight[row] : 1.0f), inv = 1.0f / xs;
+      const bool twice = twice_s != 0;
+      for (int k = lane; k < K; k += 32) {
+        const int i = i_s[k];
+        if (i < 0 || off + i < s0 || off + i >= s1) continue;
+        float q = expf(q_s[k] - tlse);
+        bool first = true;
+        if (twice) {  // its first entry stores for all
+          q = 0.0f;
+          for (int j = 0; j < K; ++j)
+            if (i_s[j] == i) {
+              first = first && j >= k;
+              q += expf(q_s[j] - tlse);
+            }
+        }
+        const float t = CAP ? tanh_of(z_s[k] * inv_cap) : z_s[k];
+        if (first) store1(off + i, (ex2(fmaf(t, kx, -xm)) * inv - q) * w * slope(t));
+      }
+    }
+  }
+  if (warp == 0 && rank == 0) {
+    const float tlse = tlse_s, xlse = logf(xs);
+    float loss = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+      const float lq = q_s[k] - tlse, q = any ? expf(lq) : 0.0f;
+      if (q > 0.0f) {
+        const float t = CAP ? tanh_of(z_s[k] * inv_cap) : z_s[k];
+        loss = fmaf(q, lq - (fmaf(t, kx, -xm) * 0.6931471805599453f - xlse), loss);
+      }
+    }
+    loss = warp_sum(loss);
+    if (lane == 0) p.loss[row] = any ? p.tau * p.tau * loss : 0.0f;
   }
 }
 
@@ -321,7 +338,9 @@ nc_status launch_r(const DistillParams& p, int M, int cs, int slice, cudaStream_
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(cs, M - m0 < 65535 ? M - m0 : 65535);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)p.K * 8;
+    int slots = 2;
+    while (slots < 2 * p.K) slots *= 2;
+    cfg.dynamicSmemBytes = (size_t)(3 * p.K + slots) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;
@@ -330,7 +349,7 @@ nc_status launch_r(const DistillParams& p, int M, int cs, int slice, cudaStream_
     a.val.clusterDim.z = 1;
     cfg.attrs = &a;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, distill_kernel<DZ, CAP, REGS>, q, slice) != cudaSuccess) return NC_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, distill_kernel<DZ, CAP, REGS>, q, slice, slots) != cudaSuccess) return NC_ERR_CUDA;
   }
   return NC_OK;
 }

@@ -20,7 +20,8 @@
 namespace nc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;           // that hold the row
+constexpr int kBlock = kThreads + 32;  // and a warp for the teacher's entries
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DistillParams {
@@ -63,30 +64,45 @@ __device__ __forceinline__ float rcp(float x) {
 // s = u^2, as a quotient of polynomials: within 3e-8 there, one reciprocal.
 // Beyond, 1 - 2 / (e^2u + 1), whose absolute error is that of its 1.
 constexpr float kNear = 1.5f;
-__device__ __forceinline__ float tanh_near(float u) {
-  const float s = u * u;
-  const float a = fmaf(fmaf(21.0f / 10395.0f, s, 1260.0f / 10395.0f), s, 1.0f);
-  const float b = fmaf(fmaf(fmaf(1.0f / 10395.0f, s, 210.0f / 10395.0f), s, 4725.0f / 10395.0f), s, 1.0f);
-  return u * a * rcp(b);
-}
 __device__ __forceinline__ float tanh_far(float u) {
   return copysignf(fmaf(-2.0f, rcp(1.0f + ex2(2.0f * kLog2e * fabsf(u))), 1.0f), u);
 }
-__device__ __forceinline__ float tanh_of(float u) { return fabsf(u) <= kNear ? tanh_near(u) : tanh_far(u); }
 
-// The tanh of four logits; the far form only where some lane of the warp needs it.
-__device__ __forceinline__ float4 tanh4(const float4& z, float inv_cap) {
-  const float4 u = make_float4(z.x * inv_cap, z.y * inv_cap, z.z * inv_cap, z.w * inv_cap);
-  float4 t = make_float4(tanh_near(u.x), tanh_near(u.y), tanh_near(u.z), tanh_near(u.w));
-  const float m = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w)));
-  if (!(m <= kNear)) {
-    if (!(fabsf(u.x) <= kNear)) t.x = tanh_far(u.x);
-    if (!(fabsf(u.y) <= kNear)) t.y = tanh_far(u.y);
-    if (!(fabsf(u.z) <= kNear)) t.z = tanh_far(u.z);
-    if (!(fabsf(u.w) <= kNear)) t.w = tanh_far(u.w);
+// tanh(z / cap) with the quotient's coefficients in terms of z.
+struct Tanh {
+  float inv_cap, near, a1, a2, b1, b2, b3;
+  __device__ explicit Tanh(float cap) {
+    inv_cap = 1.0f / cap;
+    near = kNear * cap;
+    const float c2 = inv_cap * inv_cap;
+    a1 = 1260.0f / 10395.0f * c2;
+    a2 = 21.0f / 10395.0f * (c2 * c2);
+    b1 = 4725.0f / 10395.0f * c2;
+    b2 = 210.0f / 10395.0f * (c2 * c2);
+    b3 = 1.0f / 10395.0f * (c2 * c2 * c2);
   }
-  return t;
-}
+  __device__ __forceinline__ float close(float z) const {
+    const float s = z * z;
+    const float a = fmaf(fmaf(a2, s, a1), s, 1.0f);
+    const float b = fmaf(fmaf(fmaf(b3, s, b2), s, b1), s, 1.0f);
+    return z * inv_cap * a * rcp(b);
+  }
+  __device__ __forceinline__ float operator()(float z) const {
+    return fabsf(z) <= near ? close(z) : tanh_far(z * inv_cap);
+  }
+  // four at a time; the far form only where some lane of the warp needs it
+  __device__ __forceinline__ float4 operator()(const float4& z) const {
+    float4 t = make_float4(close(z.x), close(z.y), close(z.z), close(z.w));
+    const float m = fmaxf(fmaxf(fabsf(z.x), fabsf(z.y)), fmaxf(fabsf(z.z), fabsf(z.w)));
+    if (!(m <= near)) {
+      if (!(fabsf(z.x) <= near)) t.x = tanh_far(z.x * inv_cap);
+      if (!(fabsf(z.y) <= near)) t.y = tanh_far(z.y * inv_cap);
+      if (!(fabsf(z.z) <= near)) t.z = tanh_far(z.z * inv_cap);
+      if (!(fabsf(z.w) <= near)) t.w = tanh_far(z.w * inv_cap);
+    }
+    return t;
+  }
+};
 
 // (maximum, sum) of two parts of a softmax, log2 domain.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
@@ -101,19 +117,22 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 // 256 threads share an SM, at different points of different rows: one loads
 // while another computes or stores.  The threads' (maximum, sum) are joined over
 // the block and, through distributed shared memory, over the cluster, in a fixed
-// order.  The teacher's entries are one warp's business: with K = 64 beside 8192
-// logits, eight warps repeating it took as many instructions as the row.
+// order.  The teacher's entries are the business of a warp of its own: with K = 64 beside
+// 8192 logits, eight warps repeating it took as many instructions as the row.
 // REGS = 0: longer rows, one CTA, read again from L2 for each use.
 // Groups of four start at 16-byte boundaries of z's row (the ends and a dz that is
 // not aligned alike go by single elements).
 // DZ: 0 none, 1 fp32, 2 bf16, 3 fp16
-template <int DZ, bool CAP, int REGS>
-__global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
-    distill_kernel(const DistillParams p, int slice, int slots) {
-  extern __shared__ float q_s[];  // [K] logits, then probabilities; [K] z of the entry; [K] indices; [slots]
-  __shared__ float2 part[8], part_w[kThreads / 32];
-  __shared__ float tlse_s;
-  __shared__ int any_s, twice_s;
+struct Shared {
+  float2 part[8], part_w[kThreads / 32];
+  float tlse;
+  int any, twice;
+};
+
+// FULL: every thread has REGS whole groups (no test of a group's place).
+template <int DZ, bool CAP, int REGS, bool FULL>
+__device__ __forceinline__ void distill_part(const DistillParams& p, int slice, int slots, float* q_s, Shared& sh) {
+  //  // [K] logits, then probabilities; [K] z of the entry; [K] indices; [slots]
   float* z_s = q_s + p.K;
   int32_t* i_s = reinterpret_cast<int32_t*>(z_s + p.K);
   int32_t* table = i_s + p.K;
@@ -125,12 +144,11 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
   const float* z = zr - off;
   const int end = off + V;
   const int s0 = rank * slice, s1 = min(end, s0 + slice);  // this CTA's positions
-  if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const float inv_tau = 1.0f / p.tau;
-  const float cap = p.cap, inv_cap = CAP ? 1.0f / cap : 0.0f;
-  const float kx = (CAP ? cap : 1.0f) * inv_tau * kLog2e;  // x (log2) of t or z
+  const Tanh tanh_of(CAP ? p.cap : 1.0f);
+  const float kx = (CAP ? p.cap : 1.0f) * inv_tau * kLog2e;  // x (log2) of t or z
   auto load = [&](int j) -> float4 {
-    if (j >= off && j + 4 <= end) return __ldcs(reinterpret_cast<const float4*>(z + j));
+    if (FULL || (j >= off && j + 4 <= end)) return __ldcs(reinterpret_cast<const float4*>(z + j));
     float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     if (j >= off && j < end) v.x = z[j];
     if (j + 1 >= off && j + 1 < end) v.y = z[j + 1];
@@ -140,21 +158,22 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
   };
   constexpr int STEP = kThreads * 4;
   const int j_first = s0 + tid * 4;
-  const int nr = (s1 - j_first + STEP - 1) / STEP;  // groups of this thread (0 or less: none)
+  // groups of this thread (0 or less: none)
+  const int nr = warp == kThreads / 32 ? 0 : (s1 - j_first + STEP - 1) / STEP;
   float4 keep[REGS > 0 ? REGS : 1];
   if constexpr (REGS > 0) {
 #pragma unroll
     for (int r = 0; r < REGS; ++r)
-      if (r < nr) keep[r] = load(j_first + r * STEP);
+      if (FULL ? warp < kThreads / 32 : r < nr) keep[r] = load(j_first + r * STEP);
   }
   auto each = [&](auto f) {
     if constexpr (REGS > 0) {
 #pragma unroll
       for (int r = 0; r < REGS; ++r)
-        if (r < nr) f(j_first + r * STEP, keep[r]);
+        if (FULL || r < nr) f(j_first + r * STEP, keep[r]);
     } else {
 #pragma unroll 1
-      for (int j = j_first; j < s1; j += STEP) {
+      for (int j = j_first, r = 0; r < nr; ++r, j += STEP) {
         float4 v = load(j);
         f(j, v);
       }
@@ -162,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
   };
 
   // the teacher's softmax, while the row is on its way
-  if (warp == 0) {
+  const bool helper = warp == kThreads / 32;
+  if (helper) {
     float tm = -INFINITY;
     for (int k = lane; k < slots; k += 32) table[k] = -1;
     for (int k = lane; k < K; k += 32) {
@@ -196,9 +216,9 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
       twice = __any_sync(0xffffffffu, twice);
     }
     if (lane == 0) {
-      any_s = any;
-      twice_s = twice;
-      tlse_s = any ? tm + logf(ts) : 0.0f;
+      sh.any = any;
+      sh.twice = twice;
+      sh.tlse = any ? tm + logf(ts) : 0.0f;
     }
   }
 
@@ -207,10 +227,11 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
   auto sum4 = [&](const float4& v, float m) {
     return (ex2(fmaf(v.x, kx, -m)) + ex2(fmaf(v.y, kx, -m))) + (ex2(fmaf(v.z, kx, -m)) + ex2(fmaf(v.w, kx, -m)));
   };
+  if (!helper) {
   each([&](int j, float4& v) {
     if (CAP) {
-      v = tanh4(v, inv_cap);
-      if (j < off || j + 4 > end) {  // positions outside the row stay -inf
+      v = tanh_of(v);
+      if (!FULL && (j < off || j + 4 > end)) {  // positions outside the row stay -inf
         if (j < off || j >= end) v.x = -INFINITY;
         if (j + 1 < off || j + 1 >= end) v.y = -INFINITY;
         if (j + 2 < off || j + 2 >= end) v.z = -INFINITY;
@@ -232,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     ms = join(ms, make_float2(__shfl_xor_sync(0xffffffffu, ms.x, o), __shfl_xor_sync(0xffffffffu, ms.y, o)));
-  if (lane == 0) part_w[warp] = ms;
+  if (lane == 0) sh.part_w[warp] = ms;
+  }
   __syncthreads();
   auto join_lanes = [&](const float2* v, int n) {  // n <= 8 parts, in a fixed tree
     float2 x = lane < n ? v[lane] : make_float2(-INFINITY, 0.0f);
@@ -241,18 +263,18 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
       x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
     return make_float2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0));
   };
-  ms = join_lanes(part_w, kThreads / 32);
+  ms = join_lanes(sh.part_w, kThreads / 32);
   if (CS > 1) {
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
     if (tid < CS)
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(&part[rank]), tid)),
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(&sh.part[rank]), tid)),
                    "f"(ms.x), "f"(ms.y)
                    : "memory");
     cluster_sync();
-    ms = join_lanes(part, CS);
+    ms = join_lanes(sh.part, CS);
   }
   const float xm = ms.x, xs = ms.y;
-  const bool any = any_s != 0;
+  const bool any = sh.any != 0;
 
   auto slope = [&](float t) { return CAP ? fmaf(-t, t, 1.0f) : 1.0f; };
   if constexpr (DZ != 0) {
@@ -266,12 +288,12 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
       else
         reinterpret_cast<uint16_t*>(dr)[j] = (uint16_t)Half<DZ == 3>::pack2(v, 0.0f);
     };
-    if (any) {
+    if (any && !helper) {
       each([&](int j, float4& v) {
-        const float4 t = CAP && REGS == 0 ? tanh4(v, inv_cap) : v;
+        const float4 t = CAP && REGS == 0 ? tanh_of(v) : v;
         const float4 d = make_float4(ex2(fmaf(t.x, kx, -xm)) * (wp * slope(t.x)), ex2(fmaf(t.y, kx, -xm)) * (wp * slope(t.y)),
                                      ex2(fmaf(t.z, kx, -xm)) * (wp * slope(t.z)), ex2(fmaf(t.w, kx, -xm)) * (wp * slope(t.w)));
-        if (vec && j >= off && j + 4 <= end) {
+        if (vec && (FULL || (j >= off && j + 4 <= end))) {
           if constexpr (DZ == 1)
             __stcs(reinterpret_cast<float4*>(dr + (int64_t)j * 4), d);
           else
@@ -284,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
           if (j + 3 >= off && j + 3 < end) store1(j + 3, d.w);
         }
       });
-    } else {
-      for (int j = max(s0, off) + tid; j < s1; j += kThreads) store1(j, 0.0f);
+    } else if (!any) {
+      for (int j = max(s0, off) + tid; j < s1; j += kBlock) store1(j, 0.0f);
     }
     __syncthreads();
-    if (warp == 0 && any) {  // the teacher's entries of this CTA's positions, over what was stored
-      const float tlse = tlse_s, w = p.tau * (p.weight ? p.weight[row] : 1.0f), inv = 1.0f / xs;
-      const bool twice = twice_s != 0;
+    if (helper && any) {  // the teacher's entries of this CTA's positions, over what was stored
+      const float tlse = sh.tlse, w = p.tau * (p.weight ? p.weight[row] : 1.0f), inv = 1.0f / xs;
+      const bool twice = sh.twice != 0;
       for (int k = lane; k < K; k += 32) {
         const int i = i_s[k];
         if (i < 0 || off + i < s0 || off + i >= s1) continue;
@@ -304,24 +326,38 @@ __global__ void __launch_bounds__(kThreads, REGS == 8 ? 4 : 1)
               q += expf(q_s[j] - tlse);
             }
         }
-        const float t = CAP ? tanh_of(z_s[k] * inv_cap) : z_s[k];
+        const float t = CAP ? tanh_of(z_s[k]) : z_s[k];
         if (first) store1(off + i, (ex2(fmaf(t, kx, -xm)) * inv - q) * w * slope(t));
       }
     }
   }
-  if (warp == 0 && rank == 0) {
-    const float tlse = tlse_s, xlse = logf(xs);
+  if (helper && rank == 0) {
+    const float tlse = sh.tlse, xlse = logf(xs);
     float loss = 0.0f;
     for (int k = lane; k < K; k += 32) {
       const float lq = q_s[k] - tlse, q = any ? expf(lq) : 0.0f;
       if (q > 0.0f) {
-        const float t = CAP ? tanh_of(z_s[k] * inv_cap) : z_s[k];
+        const float t = CAP ? tanh_of(z_s[k]) : z_s[k];
         loss = fmaf(q, lq - (fmaf(t, kx, -xm) * 0.6931471805599453f - xlse), loss);
       }
     }
     loss = warp_sum(loss);
     if (lane == 0) p.loss[row] = any ? p.tau * p.tau * loss : 0.0f;
   }
+}
+
+template <int DZ, bool CAP, int REGS>
+__global__ void __launch_bounds__(kBlock, REGS == 8 ? 4 : 1)
+    distill_kernel(const DistillParams p, int slice, int slots) {
+  extern __shared__ float q_s[];
+  __shared__ Shared sh;
+  if (gridDim.x > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int off = (int)((reinterpret_cast<uintptr_t>(p.z + (int64_t)blockIdx.y * p.V) >> 2) & 3);
+  const int s0 = blockIdx.x * slice;
+  if (REGS == 8 && s0 >= off && s0 + REGS * 4 * kThreads <= off + p.V)
+    distill_part<DZ, CAP, REGS, true>(p, slice, slots, q_s, sh);
+  else
+    distill_part<DZ, CAP, REGS, false>(p, slice, slots, q_s, sh);
 }
 
 template <int DZ, bool CAP, int REGS>
@@ -337,7 +373,7 @@ nc_status launch_r(const DistillParams& p, int M, int cs, int slice, cudaStream_
     if (q.dz) q.dz = static_cast<uint8_t*>(p.dz) + at * p.V * (DZ == 1 ? 4 : 2);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(cs, M - m0 < 65535 ? M - m0 : 65535);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kBlock);
     int slots = 2;
     while (slots < 2 * p.K) slots *= 2;
     cfg.dynamicSmemBytes = (size_t)(3 * p.K + slots) * 4;
@@ -362,7 +398,7 @@ nc_status launch_t(const DistillParams& p, int M, cudaStream_t stream) {
   if (groups <= kThreads) return launch_r<DZ, CAP, 1>(p, M, 1, 4 * kThreads, stream);
   if (groups <= 4 * kThreads) return launch_r<DZ, CAP, 4>(p, M, 1, 16 * kThreads, stream);
   const int cs = (groups + 8 * kThreads - 1) / (8 * kThreads);
-  if (cs <= 8) return launch_r<DZ, CAP, 8>(p, M, cs, (groups + cs - 1) / cs * 4, stream);
+  if (cs <= 8) return launch_r<DZ, CAP, 8>(p, M, cs, 32 * kThreads, stream);
   return launch_r<DZ, CAP, 0>(p, M, 1, 4 * groups, stream);
 }
 

@@ -75,17 +75,17 @@ struct Tanh {
     inv_cap = 1.0f / cap;
     near = kNear * cap;
     const float c2 = inv_cap * inv_cap;
-    a1 = 1260.0f / 10395.0f * c2;
-    a2 = 21.0f / 10395.0f * (c2 * c2);
+    a1 = 1260.0f / 10395.0f * (c2 * inv_cap);
+    a2 = 21.0f / 10395.0f * (c2 * c2 * inv_cap);
     b1 = 4725.0f / 10395.0f * c2;
     b2 = 210.0f / 10395.0f * (c2 * c2);
     b3 = 1.0f / 10395.0f * (c2 * c2 * c2);
   }
   __device__ __forceinline__ float close(float z) const {
     const float s = z * z;
-    const float a = fmaf(fmaf(a2, s, a1), s, 1.0f);
+    const float a = fmaf(fmaf(a2, s, a1), s, inv_cap);
     const float b = fmaf(fmaf(fmaf(b3, s, b2), s, b1), s, 1.0f);
-    return z * inv_cap * a * rcp(b);
+    return z * a * rcp(b);
   }
   __device__ __forceinline__ float operator()(float z) const {
     return fabsf(z) <= near ? close(z) : tanh_far(z * inv_cap);
@@ -125,9 +125,14 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 // DZ: 0 none, 1 fp32, 2 bf16, 3 fp16
 struct Shared {
   float2 part[8], part_w[kThreads / 32];
-  float tlse;
-  int any, twice;
+  uint64_t bar;  // the cluster's parts have arrived
 };
+
+// bar.sync / bar.arrive on a barrier of the CTA that not all its threads take part in
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void named_arrive(int id, int n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
 
 // FULL: every thread has REGS whole groups (no test of a group's place).
 template <int DZ, bool CAP, int REGS, bool FULL>
@@ -182,6 +187,8 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
 
   // the teacher's softmax, while the row is on its way
   const bool helper = warp == kThreads / 32;
+  bool t_any = true, t_twice = false;  // the helper's
+  float t_lse = 0.0f;
   if (helper) {
     float tm = -INFINITY;
     for (int k = lane; k < slots; k += 32) table[k] = -1;
@@ -215,11 +222,9 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
       }
       twice = __any_sync(0xffffffffu, twice);
     }
-    if (lane == 0) {
-      sh.any = any;
-      sh.twice = twice;
-      sh.tlse = any ? tm + logf(ts) : 0.0f;
-    }
+    t_any = any;
+    t_twice = twice;
+    t_lse = any ? tm + logf(ts) : 0.0f;
   }
 
   // the student's softmax: with registers, t takes the place of z
@@ -228,34 +233,33 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
     return (ex2(fmaf(v.x, kx, -m)) + ex2(fmaf(v.y, kx, -m))) + (ex2(fmaf(v.z, kx, -m)) + ex2(fmaf(v.w, kx, -m)));
   };
   if (!helper) {
-  each([&](int j, float4& v) {
-    if (CAP) {
-      v = tanh_of(v);
-      if (!FULL && (j < off || j + 4 > end)) {  // positions outside the row stay -inf
-        if (j < off || j >= end) v.x = -INFINITY;
-        if (j + 1 < off || j + 1 >= end) v.y = -INFINITY;
-        if (j + 2 < off || j + 2 >= end) v.z = -INFINITY;
-        if (j + 3 < off || j + 3 >= end) v.w = -INFINITY;
+    each([&](int j, float4& v) {
+      if (CAP) {
+        v = tanh_of(v);
+        if (!FULL && (j < off || j + 4 > end)) {  // positions outside the row stay -inf
+          if (j < off || j >= end) v.x = -INFINITY;
+          if (j + 1 < off || j + 1 >= end) v.y = -INFINITY;
+          if (j + 2 < off || j + 2 >= end) v.z = -INFINITY;
+          if (j + 3 < off || j + 3 >= end) v.w = -INFINITY;
+        }
       }
+      const float m = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+      if (REGS > 0) {
+        ms.x = fmaxf(ms.x, m);
+      } else {
+        const float mn = fmaxf(ms.x, m * kx);
+        if (mn != -INFINITY) ms = make_float2(mn, ms.y * ex2(ms.x - mn) + sum4(v, mn));
+      }
+    });
+    if constexpr (REGS > 0) {
+      ms.x *= kx;
+      if (ms.x != -INFINITY) each([&](int, float4& v) { ms.y += sum4(v, ms.x); });
     }
-    const float m = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-    if (REGS > 0) {
-      ms.x = fmaxf(ms.x, m);
-    } else {
-      const float mn = fmaxf(ms.x, m * kx);
-      if (mn != -INFINITY) ms = make_float2(mn, ms.y * ex2(ms.x - mn) + sum4(v, mn));
-    }
-  });
-  if constexpr (REGS > 0) {
-    ms.x *= kx;
-    if (ms.x != -INFINITY) each([&](int, float4& v) { ms.y += sum4(v, ms.x); });
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    ms = join(ms, make_float2(__shfl_xor_sync(0xffffffffu, ms.x, o), __shfl_xor_sync(0xffffffffu, ms.y, o)));
-  if (lane == 0) sh.part_w[warp] = ms;
+    for (int o = 16; o > 0; o >>= 1)
+      ms = join(ms, make_float2(__shfl_xor_sync(0xffffffffu, ms.x, o), __shfl_xor_sync(0xffffffffu, ms.y, o)));
+    if (lane == 0) sh.part_w[warp] = ms;
   }
-  __syncthreads();
   auto join_lanes = [&](const float2* v, int n) {  // n <= 8 parts, in a fixed tree
     float2 x = lane < n ? v[lane] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
@@ -263,22 +267,38 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
       x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
     return make_float2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0));
   };
-  ms = join_lanes(sh.part_w, kThreads / 32);
-  if (CS > 1) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
-    if (tid < CS)
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(&sh.part[rank]), tid)),
-                   "f"(ms.x), "f"(ms.y)
-                   : "memory");
-    cluster_sync();
-    ms = join_lanes(sh.part, CS);
+  // The row's warps meet (the helper is not waited for), and warp 0 sends the CTA's
+  // part to every CTA of the cluster; each waits for all of them to arrive.
+  if (!helper) {
+    named_sync(1, kThreads);
+    if (warp == 0) {
+      ms = join_lanes(sh.part_w, kThreads / 32);
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
+      if (lane < CS)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                         mapa_shared(smem_u32(&sh.part[rank]), lane)),
+                     "l"(((uint64_t)__float_as_uint(ms.y) << 32) | __float_as_uint(ms.x)),
+                     "r"(mapa_shared(smem_u32(&sh.bar), lane))
+                     : "memory");
+    }
   }
+  if (warp != 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  {
+    const uint64_t t0 = global_timer_ns();
+    bool late = false;
+    while (!late && !mbar_try_wait_cluster(smem_u32(&sh.bar), 0)) late = global_timer_ns() - t0 > kWaitLimitNs;
+    if (__any_sync(0xffffffffu, late)) {  // a CTA of the cluster never came: nothing is written
+      if (lane == 0 && p.status) atomicOr(p.status, NC_DEV_TIMEOUT);
+      if (DZ != 0 && !helper) named_arrive(2, kBlock);
+      return;
+    }
+  }
+  ms = join_lanes(sh.part, CS);
   const float xm = ms.x, xs = ms.y;
-  const bool any = sh.any != 0;
 
   auto slope = [&](float t) { return CAP ? fmaf(-t, t, 1.0f) : 1.0f; };
   if constexpr (DZ != 0) {
-    const float wp = any ? p.tau * (p.weight ? p.weight[row] : 1.0f) / xs : 0.0f;
+    const float wp = p.tau * (p.weight ? p.weight[row] : 1.0f) / xs;
     constexpr int ES = DZ == 1 ? 4 : 2;
     uint8_t* dr = static_cast<uint8_t*>(p.dz) + row * V * ES - (int64_t)off * ES;  // position 0
     const bool vec = (reinterpret_cast<uintptr_t>(dr) & (4 * ES - 1)) == 0;
@@ -288,7 +308,7 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
       else
         reinterpret_cast<uint16_t*>(dr)[j] = (uint16_t)Half<DZ == 3>::pack2(v, 0.0f);
     };
-    if (any && !helper) {
+    if (!helper) {
       each([&](int j, float4& v) {
         const float4 t = CAP && REGS == 0 ? tanh_of(v) : v;
         const float4 d = make_float4(ex2(fmaf(t.x, kx, -xm)) * (wp * slope(t.x)), ex2(fmaf(t.y, kx, -xm)) * (wp * slope(t.y)),
@@ -306,14 +326,14 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
           if (j + 3 >= off && j + 3 < end) store1(j + 3, d.w);
         }
       });
-    } else if (!any) {
-      for (int j = max(s0, off) + tid; j < s1; j += kBlock) store1(j, 0.0f);
-    }
-    __syncthreads();
-    if (helper && any) {  // the teacher's entries of this CTA's positions, over what was stored
-      const float tlse = sh.tlse, w = p.tau * (p.weight ? p.weight[row] : 1.0f), inv = 1.0f / xs;
-      const bool twice = sh.twice != 0;
-      for (int k = lane; k < K; k += 32) {
+      named_arrive(2, kBlock);
+    } else {
+      named_sync(2, kBlock);  // the row is stored; the teacher's entries go over it
+      const float tlse = t_lse, w = p.tau * (p.weight ? p.weight[row] : 1.0f), inv = 1.0f / xs;
+      if (!t_any)  // no entry: no gradient
+        for (int j = max(s0, off) + lane; j < s1; j += 32) store1(j, 0.0f);
+      const bool twice = t_twice;
+      for (int k = lane; k < K && t_any; k += 32) {
         const int i = i_s[k];
         if (i < 0 || off + i < s0 || off + i >= s1) continue;
         float q = expf(q_s[k] - tlse);
@@ -332,7 +352,8 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
     }
   }
   if (helper && rank == 0) {
-    const float tlse = sh.tlse, xlse = logf(xs);
+    const bool any = t_any;
+    const float tlse = t_lse, xlse = logf(xs);
     float loss = 0.0f;
     for (int k = lane; k < K; k += 32) {
       const float lq = q_s[k] - tlse, q = any ? expf(lq) : 0.0f;
@@ -351,7 +372,13 @@ __global__ void __launch_bounds__(kBlock, REGS == 8 ? 4 : 1)
     distill_kernel(const DistillParams p, int slice, int slots) {
   extern __shared__ float q_s[];
   __shared__ Shared sh;
-  if (gridDim.x > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&sh.bar), 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(smem_u32(&sh.bar), gridDim.x * 8);
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int off = (int)((reinterpret_cast<uintptr_t>(p.z + (int64_t)blockIdx.y * p.V) >> 2) & 3);
   const int s0 = blockIdx.x * slice;
   if (REGS == 8 && s0 >= off && s0 + REGS * 4 * kThreads <= off + p.V)
@@ -384,7 +411,7 @@ nc_status launch_r(const DistillParams& p, int M, int cs, int slice, cudaStream_
     a.val.clusterDim.y = 1;
     a.val.clusterDim.z = 1;
     cfg.attrs = &a;
-    cfg.numAttrs = cs > 1 ? 1 : 0;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, distill_kernel<DZ, CAP, REGS>, q, slice, slots) != cudaSuccess) return NC_ERR_CUDA;
   }
   return NC_OK;

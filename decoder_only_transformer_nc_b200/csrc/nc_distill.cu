@@ -24,18 +24,6 @@ constexpr int kThreads = 256;           // that hold the row
 constexpr int kBlock = kThreads + 32;  // and a warp for the teacher's entries
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct DistillParams {
-  const float* z;         // [M][V]
-  const int32_t* idx;     // [M][K]
-  const float* teacher;   // [M][K]
-  const float* weight;    // [M] or null
-  float* loss;            // [M]
-  void* dz;               // [M][V] or null
-  int V, K;
-  float cap, tau;
-  uint32_t* status;
-};
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -71,7 +59,7 @@ __device__ __forceinline__ float tanh_far(float u) {
 // tanh(z / cap) with the quotient's coefficients in terms of z.
 struct Tanh {
   float inv_cap, near, a1, a2, b1, b2, b3;
-  __device__ explicit Tanh(float cap) {
+  explicit Tanh(float cap) {
     inv_cap = 1.0f / cap;
     near = kNear * cap;
     const float c2 = inv_cap * inv_cap;
@@ -102,6 +90,19 @@ struct Tanh {
     }
     return t;
   }
+};
+
+struct DistillParams {
+  const float* z;         // [M][V]
+  const int32_t* idx;     // [M][K]
+  const float* teacher;   // [M][K]
+  const float* weight;    // [M] or null
+  float* loss;            // [M]
+  void* dz;               // [M][V] or null
+  int V, K;
+  float tau, inv_tau, kx;  // kx: x (log2) of t or z, that is cap log2(e) / tau or log2(e) / tau
+  Tanh tanh_of;            // on the host, so its coefficients are constant operands, not registers
+  uint32_t* status;
 };
 
 // (maximum, sum) of two parts of a softmax, log2 domain.
@@ -149,9 +150,8 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
   const float* z = zr - off;
   const int end = off + V;
   const int s0 = rank * slice, s1 = min(end, s0 + slice);  // this CTA's positions
-  const float inv_tau = 1.0f / p.tau;
-  const Tanh tanh_of(CAP ? p.cap : 1.0f);
-  const float kx = (CAP ? p.cap : 1.0f) * inv_tau * kLog2e;  // x (log2) of t or z
+  const Tanh& tanh_of = p.tanh_of;
+  const float kx = p.kx;
   auto load = [&](int j) -> float4 {
     if (FULL || (j >= off && j + 4 <= end)) return __ldcs(reinterpret_cast<const float4*>(z + j));
     float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
@@ -198,7 +198,7 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
         if (p.status) atomicOr(p.status, NC_DEV_TARGET_RANGE);
         i = -1;
       }
-      const float t = i < 0 ? -INFINITY : p.teacher[row * K + k] * inv_tau;
+      const float t = i < 0 ? -INFINITY : p.teacher[row * K + k] * p.inv_tau;
       z_s[k] = i < 0 ? 0.0f : zr[i];
       i_s[k] = i;
       q_s[k] = t;
@@ -284,9 +284,12 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
   }
   if (warp != 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   {
-    const uint64_t t0 = global_timer_ns();
     bool late = false;
-    while (!late && !mbar_try_wait_cluster(smem_u32(&sh.bar), 0)) late = global_timer_ns() - t0 > kWaitLimitNs;
+    if (!mbar_try_wait_cluster(smem_u32(&sh.bar), 0)) {
+      const uint64_t t0 = global_timer_ns();
+      for (uint32_t it = 1; !late && !mbar_try_wait_cluster(smem_u32(&sh.bar), 0); ++it)
+        if ((it & 255u) == 0u) late = global_timer_ns() - t0 > kWaitLimitNs;
+    }
     if (__any_sync(0xffffffffu, late)) {  // a CTA of the cluster never came: nothing is written
       if (lane == 0 && p.status) atomicOr(p.status, NC_DEV_TIMEOUT);
       if (DZ != 0 && !helper) named_arrive(2, kBlock);
@@ -430,8 +433,8 @@ nc_status launch_t(const DistillParams& p, int M, cudaStream_t stream) {
 }
 
 template <int DZ>
-nc_status launch_c(const DistillParams& p, int M, cudaStream_t stream) {
-  return p.cap > 0.0f ? launch_t<DZ, true>(p, M, stream) : launch_t<DZ, false>(p, M, stream);
+nc_status launch_c(const DistillParams& p, int M, float cap, cudaStream_t stream) {
+  return cap > 0.0f ? launch_t<DZ, true>(p, M, stream) : launch_t<DZ, false>(p, M, stream);
 }
 
 }  // namespace
@@ -440,12 +443,13 @@ nc_status distill_topk_launch(const float* z, const int32_t* idx, const float* t
                               float* loss, void* dz, int dz_kind, int M, int V, int K, float tau, float cap,
                               uint32_t* dev_status, cudaStream_t stream) {
   if (M == 0) return NC_OK;
-  const DistillParams p{z, idx, teacher, weight, loss, dz, V, K, cap, tau, dev_status};
+  const DistillParams p{z, idx, teacher, weight, loss, dz, V, K, tau, 1.0f / tau, (cap > 0.0f ? cap : 1.0f) / tau * kLog2e,
+                        Tanh(cap > 0.0f ? cap : 1.0f), dev_status};
   switch (dz_kind) {
-    case 0: return launch_c<0>(p, M, stream);
-    case 1: return launch_c<1>(p, M, stream);
-    case 2: return launch_c<2>(p, M, stream);
-    default: return launch_c<3>(p, M, stream);
+    case 0: return launch_c<0>(p, M, cap, stream);
+    case 1: return launch_c<1>(p, M, cap, stream);
+    case 2: return launch_c<2>(p, M, cap, stream);
+    default: return launch_c<3>(p, M, cap, stream);
   }
 }
 

@@ -278,7 +278,7 @@ __device__ __forceinline__ uint64_t code_of(float l, int pos) {
   return ((uint64_t)key_of(l) << 32) | (uint32_t)~pos;
 }
 
-constexpr int kStageBytes = 160 * 1024;  // rows up to this are staged in shared memory
+constexpr int kStageBytes = 180 * 1024;  // a staged row and the list before it
 constexpr int kTopBins = 256;  // histogram of the threads' maxima
 
 template <int NT>
@@ -298,7 +298,6 @@ struct Smem {
     } s;
   };
   uint64_t cand[NT];
-  uint64_t own[NT * 2];
   uint64_t bar[NT / 32];
   int ncand, bk, cnt_bk, b1, b2, cnt_b1, cnt_b2, pick;
 };
@@ -530,6 +529,167 @@ __device__ __noinline__ bool pick_from_list(int n, int k, float tp, int64_t z_lo
       const float lt = sm.s.logit[rank];
       const double z = log((double)total) - (double)p.sh * 0.6931471805599453;
       p.logprob[row] = (float)((lt == weight.mx ? 0.0 : ((double)lt - (double)weight.mx) / (double)T) - z);
+    }
+  }
+  return true;
+}
+
+// The row's token where the tokens from `least` on, at most kPart in a warp's
+// segment, hold every kept one: one pass
+// lists them in index order and sums the others' mass; the rest happens in
+// registers, kPer tokens a thread with integer weights.  The cuts are bisections
+// over the keys.  Only the others' mass is fp32; false where its error leaves
+// top-p's cut open, or where a cut lies past the list.  For the whole block.
+constexpr int kPart = 256, kPer = kPart / 32;
+template <int NT>
+__device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float mp, float u, float T, float least, const Expo we,
+                                           uint64_t* list, Smem<NT>& sm, const SampleParams& p, int row) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool use_p = !(tp >= 1.0f);
+  const Expo32 wf(we.mx, we.c, T);
+  uint64_t* mine = list + warp * kPart;
+  int n = 0;
+  Sum2 tail;
+  float s1 = 0.0f;
+#pragma unroll 1
+  for (int j0 = r.seg0; j0 < r.seg1; j0 += 128) {
+    const int j = j0 + lane * 4;
+    const float4 v = j < r.seg1 ? load4(r, j) : make_float4(NAN, NAN, NAN, NAN);
+    const float l[4] = {v.x, v.y, v.z, v.w};
+    uint32_t bal[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bal[e] = __ballot_sync(0xffffffffu, l[e] >= least);
+    if (use_p && k <= 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float d;
+        float w = wf(l[e], d);
+        w = l[e] >= least ? 0.0f : w;
+        s1 = fmaf(w, d, s1);
+        tail.add(w);
+      }
+    }
+    if (bal[0] | bal[1] | bal[2] | bal[3]) {  // of the 128, a lane's four are neighbours
+      const uint32_t lt = (1u << lane) - 1u;
+      int at = n + __popc(bal[0] & lt) + __popc(bal[1] & lt) + __popc(bal[2] & lt) + __popc(bal[3] & lt);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (l[e] >= least) {
+          if (at < kPart) mine[at] = code_of(l[e], j + e);
+          ++at;
+        }
+      n += __popc(bal[0]) + __popc(bal[1]) + __popc(bal[2]) + __popc(bal[3]);
+    }
+  }
+  if (__syncthreads_or(n > kPart)) return false;
+  uint32_t key[kPer];
+  int64_t w[kPer], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int i = lane * kPer + e;
+    key[e] = i < n ? (uint32_t)(mine[i] >> 32) : 0u;
+    w[e] = i < n ? we(value_of(key[e])) : 0;
+    sum += w[e];
+  }
+  const uint32_t kmax = key_of(we.mx), kmin = key_of(least);
+  auto count_from = [&](uint32_t from) {
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) c += key[e] >= from;
+    return block_reduce<NT>(c, sm.red, Add{}, 0);
+  };
+  auto mass_above = [&](uint32_t at) {
+    int64_t c = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) c += key[e] > at ? w[e] : 0;
+    return block_reduce<NT>(c, sm.red, Add{}, (int64_t)0);
+  };
+  // kept: key > cut, and of those with key == cut the first `ties` in index order
+  uint32_t cut = 0;
+  int ties = INT_MAX;
+  if (k > 0) {
+    if (count_from(1u) < k) return false;
+    uint32_t lo = kmin, hi = kmax;  // the largest key with at least k tokens from it on
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2 + 1;
+      if (count_from(mid) >= k)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    cut = lo;
+    ties = k - count_from(cut + 1);
+  }
+  if (use_p) {
+    const double unit = (double)((int64_t)1 << p.sh), pp = tp > 0.0f ? (double)tp : 0.0;
+    double z_lo, z_hi, within;
+    if (k > 0) {
+      z_lo = z_hi = within = (double)(mass_above(cut) + (int64_t)ties * we(value_of(cut)));
+    } else {
+      within = (double)block_reduce<NT>(sum, sm.red, Add{}, (int64_t)0);
+      const double t = block_reduce<NT>(tail.value(), sm.red, Add{}, 0.0) * unit;
+      const double e = block_reduce<NT>((double)s1, sm.red, Add{}, 0.0) * we.c * unit;
+      const double err = Expo32::kErr * t - Expo32::kErrY * e;
+      z_lo = within + t - err;
+      z_hi = within + t + err;
+    }
+    const double want_lo = pp * z_lo, want_hi = pp * z_hi;
+    if (k <= 0 && !(within >= want_hi)) return false;  // the cut lies past the list
+    uint32_t lo = max(cut, kmin), hi = kmax;  // the smallest key with less than what is wanted above it
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const double s = (double)mass_above(mid);
+      if (s < want_lo)
+        hi = mid;
+      else if (s >= want_hi)
+        lo = mid + 1;
+      else
+        return false;
+    }
+    const double s = (double)mass_above(lo), wt = (double)we(value_of(lo));
+    int m = INT_MAX;  // of its ties, those with less before them
+    if (wt > 0.0) {
+      const double a = ceil((want_lo - s) / wt), b = ceil((want_hi - s) / wt);
+      if (a != b) return false;
+      m = a < 1.0 ? 1 : (int)fmin(a, 2147483647.0);
+    }
+    ties = lo == cut ? min(ties, m) : m;
+    cut = lo;
+  }
+  const int64_t wmin = mp > 0.0f ? __double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << p.sh)) : 0;
+  int mt = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) mt += key[e] == cut && cut != 0u;
+  int64_t seen = block_scan<NT>((int64_t)mt, sm.red) - mt;
+  sum = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const bool tie = key[e] == cut;
+    const bool keep = key[e] > cut || (tie && seen < ties);
+    seen += tie;
+    if (!keep || w[e] < wmin) w[e] = 0;
+    sum += w[e];
+  }
+  const int64_t inc = block_scan<NT>(sum, sm.red);
+  if (tid == NT - 1) sm.seg[0] = inc;
+  __syncthreads();
+  const int64_t total = sm.seg[0];
+  const double target = (u > 0.0f ? (double)u : 0.0) * (double)total;
+  const bool last = target >= (double)total;  // u >= 1: the last kept token
+  if (sum > 0 && (last ? inc == total : (double)inc > target && (double)(inc - sum) <= target)) {
+    int64_t run = inc - sum;
+    int pick = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (w[e] > 0 && (last || (double)run <= target)) pick = e;
+      run += w[e];
+    }
+    const uint64_t code = mine[lane * kPer + pick];
+    p.tokens[row] = (int)~(uint32_t)code - r.off;
+    if (p.logprob) {
+      const float l = value_of((uint32_t)(code >> 32));
+      const double z = log((double)total) - (double)p.sh * 0.6931471805599453;
+      p.logprob[row] = (float)((l == we.mx ? 0.0 : ((double)l - (double)we.mx) / (double)T) - z);
     }
   }
   return true;
@@ -839,7 +999,8 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
 template <int NT, bool STAGED>
 __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const SampleParams p) {
   __shared__ Smem<NT> sm;
-  extern __shared__ __align__(16) float staged[];
+  extern __shared__ __align__(16) uint64_t list[];  // [NT / 32 * kPart], then the staged row
+  float* staged = reinterpret_cast<float*>(list + NT / 32 * kPart);
   constexpr int NW = NT / 32;
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float* x = p.logits + (int64_t)row * p.ld;
@@ -970,7 +1131,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       // a value at or below every one in the bins up to it (a little lower: it was
       // fp32 arithmetic that put them there)
       const float edge = mx - ((float)bstar + 0.51f) / q.scale - fabsf(mx) * 1e-6f;
-      const int n = q.scale > 0.0f ? collect<NT, 2>(r, sm.own, sm.cand, NT, &sm.ncand,
+      const int n = q.scale > 0.0f ? collect<NT, 2>(r, list, sm.cand, NT, &sm.ncand,
                                                     [&](float l) { return l >= edge; })
                                    : NT + 1;
       if (n <= NT) {
@@ -978,6 +1139,53 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
         return;
       }
     }
+    __syncthreads();
+  }
+
+  if (k >= p.V) k = 0;
+  if ((use_p || k > 0 || mp > 0.0f) && T <= 4.0f && Expo32::usable(mx, T)) {
+    // How far from the maximum to list: min-p's reach where that is the only filter,
+    // else what about five eighths of the list hold, judged by the first 128 tokens
+    // of every segment (in 64 steps of T / 4).  Where those tokens' likely ones hold
+    // far less than top-p's share, the list would be made in vain (10 of 60 us at
+    // 32768 tokens).
+    float least = mx + logf(fminf(mp, 1.0f)) * T * 1.00001f - 1e-5f * T - fabsf(mx) * 1e-6f;
+    bool enough = true;
+    if (use_p || k > 0) {
+      const Expo32 wf(mx, sm.c, T);
+      for (int i = tid; i < 64; i += NT) sm.h.cnt[i] = sm.h.lo[i] = 0u;
+      __syncthreads();
+      const int j = r.seg0 + lane * 4;
+      const float4 v = j < r.seg1 ? load4(r, j) : make_float4(NAN, NAN, NAN, NAN);
+      const float l[4] = {v.x, v.y, v.z, v.w};
+      uint32_t far = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float d;
+        const uint32_t m = (uint32_t)(wf(l[e], d) * 1048576.0f);
+        const float step = -d * (4.0f / T);
+        if (step < 64.0f) {
+          atomicAdd(&sm.h.cnt[(int)step], 1u);
+          atomicAdd(&sm.h.lo[(int)step], m);
+        } else {
+          far += m;
+        }
+      }
+      const int64_t rest = block_reduce<NT>((int64_t)far, sm.red, Add{}, (int64_t)0);  // (a barrier too)
+      // inclusive counts and masses, two steps a lane
+      const uint32_t c0 = sm.h.cnt[2 * lane], c1 = c0 + sm.h.cnt[2 * lane + 1];
+      const int64_t m0 = sm.h.lo[2 * lane], m1 = m0 + sm.h.lo[2 * lane + 1];
+      const int64_t cb = warp_scan((int64_t)c1) - c1, mb = warp_scan(m1) - m1, all = __shfl_sync(0xffffffffu, mb + m1, 31);
+      const int64_t most = (int64_t)(NT / 32 * kPart) * 5 / 8 * min(r.per, 128) / r.per;
+      const int steps = __reduce_add_sync(0xffffffffu, (cb + c0 <= most) + (cb + c1 <= most));
+      const int64_t near = __reduce_max_sync(0xffffffffu, (uint32_t)(cb + c1 <= most ? mb + m1 : cb + c0 <= most ? mb + m0 : 0));
+      least = mx - 0.25f * T * (float)steps;
+      const double scale = (double)r.per / min(r.per, 128);
+      enough = steps > 0 && (k > 0 ? k <= most * scale
+                                   : near * scale + 1048576.0 > 0.9 * tp * ((all + rest) * scale + 1048576.0));
+    }
+    __syncthreads();
+    if (enough && pick_from_top<NT>(r, k, tp, mp, u, T, least, weight, list, sm, p, row)) return;
     __syncthreads();
   }
 
@@ -1125,7 +1333,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       // histogram (off by less than kHist and a unit a token) settles the cut
       // unless it falls that close to a token's border.
       const float edge = Cut::kOne + (float)q.b2;  // (b2 is the last bin: what is past it weighs nothing)
-      collect<NT, 2>(r, sm.own, sm.cand, NT, &sm.ncand,
+      collect<NT, 2>(r, list, sm.cand, NT, &sm.ncand,
                      [&](float l) { return l > -INFINITY && q.fbin(l) <= edge; });
       const double per = sh >= 2 * p.half ? (double)((int64_t)1 << (sh - 2 * p.half)) : 1.0 / (double)(1 << (2 * p.half - sh));
       const int64_t z_lo = (int64_t)((double)m_all * per * (1.0 - Expo32::kHist)),
@@ -1173,10 +1381,10 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, half};
   // Rows for every SM and more: some on each SM, they load and compute in turn (from
   // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
-  if (M > device_sm_count()) return launch_t<256, false>(p, M, 0, stream);
-  const size_t smem = ((size_t)V + 7) / 4 * 16;
+  if (M > device_sm_count()) return launch_t<256, false>(p, M, 8 * kPart * 8, stream);
+  const size_t smem = 16 * kPart * 8 + ((size_t)V + 7) / 4 * 16;
   if (smem <= kStageBytes) return launch_t<512, true>(p, M, smem, stream);
-  return launch_t<512, false>(p, M, 0, stream);
+  return launch_t<512, false>(p, M, 16 * kPart * 8, stream);
 }
 
 }  // namespace nc

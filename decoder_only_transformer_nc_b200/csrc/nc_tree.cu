@@ -350,8 +350,11 @@ nc_status tree_attn_run(const TreeAttnParams& p, int B, cudaStream_t stream) {
   int keys = p.T_max;
   if (p.window > 0 && p.window - 1 < keys) keys = p.window - 1;
   const int tiles = (keys + p.N + kTK - 1) / kTK;
-  int cs = 1;  // split the keys until the CTAs fill the device twice, down to one tile a CTA
-  while (cs < 8 && cs * 2 <= tiles && (int64_t)base * cs * 2 <= 2 * device_sm_count()) cs *= 2;
+  // split the keys until the CTAs fill the device as often as their shared memory
+  // lets them share an SM, down to one tile a CTA
+  const int64_t slots = (int64_t)device_sm_count() * (227 * 1024 / (smem + 4096));
+  int cs = 1;
+  while (cs < 8 && cs * 2 <= tiles && (int64_t)base * cs * 2 <= slots) cs *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, row_tiles * p.Hkv, B);
   cfg.blockDim = dim3(128);

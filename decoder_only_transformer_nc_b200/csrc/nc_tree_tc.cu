@@ -76,13 +76,17 @@ struct Params {
   const int32_t* lens;
   const uint32_t* mask;
   uint16_t* out;
-  float* part;  // [CTAs][2 pieces][2 row tiles][D + 2][128]: O, max, sum; rows innermost
+  float* part;  // [CTAs][2 pieces][2 row tiles]: O [D / 4][128 rows][4], then max and sum [128][2]
   int B, N, H, Hkv, T_max, win;
   int G, npt, tiles_r, pairs;  // query heads a kv head, nodes a row tile, row tiles, pairs of them
   float scale_log2;
   uint32_t* dev_status;
   uint64_t limit_ns;
 };
+
+// A unit's first scores, last products and result take about as long as this many
+// more tiles; the deal counts them at its end, where they are no work.
+constexpr int kUnitCost = 2;
 
 struct Row {  // one cache row's committed keys
   int len, lo, n_c;
@@ -97,8 +101,8 @@ __device__ __forceinline__ Row row_of(const Params& p, int len) {
 }
 
 // The work in shared memory: pre[b] = linear index of row b's first tile (its
-// units one after another), pre[B] = all tiles, len[b] = the clamped lengths.
-// (Fewer than 2^31 tiles: see tree_attention_tc_fits.)
+// units one after another, kUnitCost tiles of nothing behind each), pre[B] = all
+// of them, len[b] = the clamped lengths.  (Fewer than 2^31: tree_attention_tc_fits.)
 struct Plan {
   int* pre;
   int* len;
@@ -110,7 +114,7 @@ __device__ __forceinline__ Plan make_plan(const Params& p, int* mem) {
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
     const int len = min(max(p.lens[b], 0), p.T_max);
     pl.len[b] = len;
-    pl.pre[b + 1] = (row_of(p, len).n_c + 1) * upr;
+    pl.pre[b + 1] = (row_of(p, len).n_c + 1 + kUnitCost) * upr;
   }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -141,8 +145,9 @@ struct Deal {
 
 struct Seg {
   int b, g, pair;  // the unit
-  int t0, n;       // its tiles [t0, t0 + n) ...
+  int t0, n;       // its tiles [t0, t0 + n) (n = 0: none, only the cost behind them) ...
   int units_t;     // ... of this many
+  int next;        // linear index behind the piece
   bool two;        // two row tiles (streams share the key tiles)
   int u0;          // linear index of the unit's first tile
 };
@@ -160,12 +165,14 @@ __device__ __forceinline__ Seg seg_at(const Params& p, const int* pre, int x, in
   const int upr = p.Hkv * p.pairs;
   Seg s;
   s.b = lo;
-  s.units_t = (pre[lo + 1] - pre[lo]) / upr;
-  const int rem = x - pre[lo], u = rem / s.units_t;
-  s.t0 = rem - u * s.units_t;
+  const int span = (pre[lo + 1] - pre[lo]) / upr;
+  s.units_t = span - kUnitCost;
+  const int rem = x - pre[lo], u = rem / span;
+  s.t0 = rem - u * span;
   s.pair = u % p.pairs;
   s.g = u / p.pairs;
-  s.n = min(s.units_t - s.t0, end - x);
+  s.next = min(x + span - s.t0, end);
+  s.n = max(min(s.units_t - s.t0, end - x), 0);
   s.two = 2 * s.pair + 1 < p.tiles_r;
   s.u0 = x - s.t0;
   return s;
@@ -294,8 +301,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t outstanding = 0, out_phase = 0;  // bits 0,1: K slots; 2: Q; 3,4: V slots
       int gt = 0, n = 0;                        // tiles and pieces done before
       bool ok = true;
-      for (int x = x_begin; x < x_end && ok; ++n) {
+      for (int x = x_begin; x < x_end && ok;) {
         const Seg sg = seg_at(p, pl.pre, x, x_end);
+        x = sg.next;
+        if (sg.n == 0) continue;
         const Row rw = row_of(p, pl.len[sg.b]);
         if (!mbar_wait(smem_u32(&bar->q_empty), (n & 1) ^ 1, ctl)) break;
         const int nq = sg.two ? 2 : 1;
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
         }
         gt += sg.n;
-        x += sg.n;
+        ++n;
       }
       if (!ok || bar->abort_flag) {  // let the copies in flight land
         int zero = 0;
@@ -351,8 +360,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int gt = 0, n = 0;
     int gp[2] = {0, 0};  // P V products issued for each stream
     bool ok = true;
-    for (int x = x_begin; x < x_end && ok; ++n) {
+    for (int x = x_begin; x < x_end && ok;) {
       const Seg sg = seg_at(p, pl.pre, x, x_end);
+      x = sg.next;
+      if (sg.n == 0) continue;
       const int sn = __shfl_sync(0xffffffffu, sg.n, 0);
       const bool two = __shfl_sync(0xffffffffu, (int)sg.two, 0) != 0;
       if (!mbar_wait(smem_u32(&bar->q_full), n & 1, ctl)) break;
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       gt += sn;
-      x += sn;
+      ++n;
     }
     if (elect_one()) umma_commit(smem_u32(&bar->drain));
     __syncwarp();
@@ -425,8 +436,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int W = (p.N + 31) / 32;
     int gt = 0, n = 0, gs = 0, go[2] = {0, 0};
     bool ok = true;
-    for (int x = x_begin; x < x_end && ok; ++n) {
+    for (int x = x_begin; x < x_end && ok;) {
       const Seg sg = seg_at(p, pl.pre, x, x_end);
+      const bool first_piece = x == x_begin;
+      x = sg.next;
+      if (sg.n == 0) continue;
       const Row rw = row_of(p, pl.len[sg.b]);
       const int my_tile = 2 * sg.pair + (sg.two ? w : 0);
       const int node = my_tile * p.npt + r / p.G;
@@ -450,6 +464,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int k = 0; k < 4; ++k) see[k] = 0u;
         }
       }
+      uint32_t used[4] = {0u, 0u, 0u, 0u};  // the row's used nodes, for the drafted tile
+      bool hole = false;
+      if (sg.t0 + sg.n > rw.n_c) {
+        uint32_t word[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k * 32 + (int)lane < p.N) word[k] = p.mask[((int64_t)sg.b * p.N + k * 32 + (int)lane) * W + k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          used[k] = __ballot_sync(0xffffffffu, (word[k] >> lane) & 1u);
+          const int left = p.N - 32 * k;
+          const uint32_t nodes = left <= 0 ? 0u : left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+          hole = hole || (used[k] & nodes) != nodes;
+        }
+      }
       const bool live_warp = __any_sync(0xffffffffu, depth >= 0);
       const int tmin = depth >= 0 ? rw.len + depth - p.win + 1 : 0;  // first visible position (unused rows: any)
       float m_used = -INFINITY, l = 0.0f;
@@ -465,17 +494,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool draft = t == rw.n_c;
         if (draft) {
           // V of unused nodes: zeros
-          uint32_t used[4] = {0u, 0u, 0u, 0u};
-          bool hole = false;
-          for (int k = 0; k < W; ++k) {
-            const int i = k * 32 + (int)lane;
-            const bool u = i < p.N && ((p.mask[((int64_t)sg.b * p.N + i) * W + k] >> lane) & 1u);
-            const uint32_t bal = __ballot_sync(0xffffffffu, u);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (q == k) used[q] = bal;
-            hole = hole || __any_sync(0xffffffffu, i < p.N && !u);
-          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) see[k] &= used[k];
           if (hole) {
@@ -628,12 +646,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // one row tile: each stream takes half of the columns of both O
       const int c_lo = sg.two ? 0 : w * (D / 64), c_hi = sg.two ? D / 32 : (w + 1) * (D / 64);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      // pieces: a warp's 32 rows are neighbours for each column, so its stores are whole lines
-      float* part = p.part + ((((int64_t)blockIdx.x * 2 + (x == x_begin ? 0 : 1)) * 2 + (sg.two ? w : 0)) * (D + 2)) * 128 + r;
-      if (!whole && c_lo == 0) {
-        part[D * 128] = depth >= 0 ? m_used : -INFINITY;
-        part[(D + 1) * 128] = depth >= 0 ? l : 0.0f;
-      }
+      // pieces: four columns of a warp's 32 rows are neighbours, so its stores are whole lines
+      float* part = p.part + (((int64_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * 2 + (sg.two ? w : 0)) * ((D + 2) * 128);
+      if (!whole && c_lo == 0)
+        *reinterpret_cast<float2*>(part + D * 128 + r * 2) =
+            make_float2(depth >= 0 ? m_used : -INFINITY, depth >= 0 ? l : 0.0f);
 #pragma unroll 1
       for (int c = c_lo; c < c_hi; ++c) {
         uint32_t ra[32];
@@ -666,14 +683,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(c * 32 + e) * 128] = v[e];
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(part + ((c * 8 + q) * 128 + r) * 4) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar->o_free));
       gt += sg.n;
-      x += sg.n;
+      ++n;
     }
   }
 
@@ -700,7 +719,7 @@ __global__ void __launch_bounds__(256) tree_tc_merge_kernel(const Params p, int 
   const Seg sg = seg_at(p, pl.pre, x, total);
   // Every CTA has a tile or more once c has one (the first ones get the extra
   // tiles), so the piece before this one is CTA c - 1's.
-  if (sg.t0 == 0 || deal.begin(c - 1) > sg.u0) return;
+  if (sg.t0 == 0 || sg.n == 0 || deal.begin(c - 1) > sg.u0) return;
   const int u_end = sg.u0 + sg.units_t;
   const int lane = threadIdx.x & 31;
   int k_end = c + 1;  // past the last piece's CTA
@@ -714,26 +733,40 @@ __global__ void __launch_bounds__(256) tree_tc_merge_kernel(const Params p, int 
     const bool in = r < p.G * p.npt && node < p.N;
     // piece k of the unit: CTA k's first piece unless the unit starts inside CTA k's work
     auto piece = [&](int k) {
-      return p.part + ((((int64_t)k * 2 + (deal.begin(k) >= sg.u0 ? 0 : 1)) * 2 + (rg >> 2)) * (D + 2)) * 128 + r;
+      return p.part + (((int64_t)k * 2 + (deal.begin(k) >= sg.u0 ? 0 : 1)) * 2 + (rg >> 2)) * ((D + 2) * 128);
     };
     float acc[16], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-    for (int k = c - 1; k < k_end; ++k) {
-      const float* src = piece(k);
-      float v[16];
+    for (int k0 = c - 1; k0 < k_end; k0 += 3) {  // three pieces' loads in flight
+      float4 v[3][4];
+      float2 ml[3];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = src[(cg * 16 + e) * 128];
-      const float mk = src[D * 128], lk = src[(D + 1) * 128];
-      const float mn = fmaxf(m, mk);
-      // rows of a piece that saw nothing (and rows that are no node's) hold anything
-      const bool got = in && mk != -INFINITY;
-      const float a = m == -INFINITY ? 0.0f : ex2f((m - mn) * p.scale_log2), b = ex2f((mk - mn) * p.scale_log2);
-      if (got) {
+      for (int i = 0; i < 3; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        if (k0 + i < k_end) {
+          const float* src = piece(k0 + i);
+          ml[i] = *reinterpret_cast<const float2*>(src + D * 128 + r * 2);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = fmaf(acc[e], a, v[e] * b);
-        l = fmaf(l, a, lk * b);
-        m = mn;
+          for (int q = 0; q < 4; ++q) v[i][q] = *reinterpret_cast<const float4*>(src + ((cg * 4 + q) * 128 + r) * 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        // rows of a piece that saw nothing (and rows that are no node's) hold anything
+        if (in && ml[i].x != -INFINITY) {
+          const float mn = fmaxf(m, ml[i].x);
+          const float a = m == -INFINITY ? 0.0f : ex2f((m - mn) * p.scale_log2), b = ex2f((ml[i].x - mn) * p.scale_log2);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[4 * q] = fmaf(acc[4 * q], a, v[i][q].x * b);
+            acc[4 * q + 1] = fmaf(acc[4 * q + 1], a, v[i][q].y * b);
+            acc[4 * q + 2] = fmaf(acc[4 * q + 2], a, v[i][q].z * b);
+            acc[4 * q + 3] = fmaf(acc[4 * q + 3], a, v[i][q].w * b);
+          }
+          l = fmaf(l, a, ml[i].y * b);
+          m = mn;
+        }
       }
     }
     if (!in) continue;
@@ -782,7 +815,7 @@ nc_status launch_t(const CUtensorMap& mq, const CUtensorMap& mc, const CUtensorM
 
 }  // namespace tree_tc
 
-// At most 2^15 units of at most 2^22 / 128 + 1 tiles: linear tile indices fit 32 bits.
+// At most 2^15 units of at most 2^22 / 128 + 3 tiles: linear tile indices fit 32 bits.
 bool tree_attention_tc_fits(int B, int N, int H, int Hkv, int window) {
   const int G = H / Hkv;
   if (G > tree_tc::BM) return false;
@@ -836,7 +869,7 @@ nc_status tree_attention_tc_launch(const uint16_t* q, int64_t q_stride, const ui
   }
   // no more CTAs than the longest rows have tiles
   const int keys = window > 0 && window - 1 < T_max ? window - 1 : T_max;
-  const int64_t most = (int64_t)B * Hkv * p.pairs * ((keys + BKV - 1) / BKV + 1);
+  const int64_t most = (int64_t)B * Hkv * p.pairs * ((keys + BKV - 1) / BKV + 1);  // (without kUnitCost)
   const int ctas = (int)(most < device_sm_count() ? most : device_sm_count());
   if (D == 128)
     return f16 ? launch_t<128, true>(mq, mc, md, p, ctas, stream) : launch_t<128, false>(mq, mc, md, p, ctas, stream);

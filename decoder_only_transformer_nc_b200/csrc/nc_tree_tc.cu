@@ -56,7 +56,8 @@ struct Geo {
   static constexpr int OFF_V = OFF_K + 2 * TILE;
   static constexpr int OFF_BAR = OFF_V + 2 * TILE;
   static constexpr int OFF_X = OFF_BAR + 256;   // (max, sum) of both streams, by piece parity [2][2][128][2]
-  static constexpr int OFF_PRE = OFF_X + 2 * 2 * 128 * 2 * 4;
+  static constexpr int OFF_SEE = OFF_X + 2 * 2 * 128 * 2 * 4;  // visible drafted keys of every softmax thread
+  static constexpr int OFF_PRE = OFF_SEE + 256 * 16;
   static constexpr int SMEM_BYTES = OFF_PRE + (2 * kMaxB + 1) * 4;
 };
 
@@ -216,6 +217,16 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
+// Inverse: thread i gets lane (base lane + i).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ uint64_t pack_u32x2(uint32_t a, uint32_t b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
@@ -256,6 +267,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* sm = smem_raw;
   Bars* bar = reinterpret_cast<Bars*>(sm + G::OFF_BAR);
   float* xval = reinterpret_cast<float*>(sm + G::OFF_X);
+  uint4* see_s = reinterpret_cast<uint4*>(sm + G::OFF_SEE);
   const uint32_t s_q = smem_u32(sm), s_k = s_q + G::OFF_K, s_v = s_q + G::OFF_V;
   const uint32_t warp = warp_id_sync();
   const uint32_t lane = lane_id();
@@ -464,9 +476,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int k = 0; k < 4; ++k) see[k] = 0u;
         }
       }
-      uint32_t used[4] = {0u, 0u, 0u, 0u};  // the row's used nodes, for the drafted tile
+      // For the drafted tile: whether the row has unused nodes, and this thread's visible
+      // keys (in shared memory: registers are short in the loop).
       bool hole = false;
       if (sg.t0 + sg.n > rw.n_c) {
+        uint32_t used[4];
         uint32_t word[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -477,7 +491,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int left = p.N - 32 * k;
           const uint32_t nodes = left <= 0 ? 0u : left >= 32 ? 0xffffffffu : (1u << left) - 1u;
           hole = hole || (used[k] & nodes) != nodes;
+          see[k] &= used[k];
         }
+        see_s[(w * 128 + r)] = make_uint4(see[0], see[1], see[2], see[3]);
       }
       const bool live_warp = __any_sync(0xffffffffu, depth >= 0);
       const int tmin = depth >= 0 ? rw.len + depth - p.win + 1 : 0;  // first visible position (unused rows: any)
@@ -494,8 +510,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool draft = t == rw.n_c;
         if (draft) {
           // V of unused nodes: zeros
-#pragma unroll
-          for (int k = 0; k < 4; ++k) see[k] &= used[k];
           if (hole) {
             const int gi = gt + j, st = gi & 1;
             if (__any_sync(0xffffffffu, !mbar_wait(smem_u32(&bar->v_full[st]), (uint32_t)(gi >> 1) & 1, ctl))) {
@@ -504,7 +518,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             bool mine = false;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mine = mine || (k == (int)quarter && r < p.N && !((used[k] >> lane) & 1u));
+            for (int k = 0; k < 4; ++k) mine = mine || (k == (int)quarter && r < p.N && !((p.mask[((int64_t)sg.b * p.N + r) * W + k] >> lane) & 1u));
             if (mine) {
               uint4* v = reinterpret_cast<uint4*>(sm + G::OFF_V + st * G::TILE + r * 128);
 #pragma unroll
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll 1
             for (int c = 0; c < BKV / 32; ++c) {
               const int fk = first_key - c * 32;
-              const uint32_t vis = draft ? (c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3])
+              const uint32_t vis = draft ? reinterpret_cast<const uint32_t*>(see_s + w * 128 + r)[c]
                                          : (fk <= 0 ? 0xffffffffu : fk >= 32 ? 0u : 0xffffffffu << fk);
               uint32_t rr[32];
               tmem_ld_32x32b_x32(scol + c * 32, rr);
@@ -539,72 +553,83 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             tmem_wait_st();
           }
-          // The scores are read twice (maximum, then weights), 32 at a time with the
-          // next 32 on their way: 128 of them in registers spill.
-          uint32_t sr[2][32];
-          float mx8[8];
+          // The weights against the maximum so far, the tile's own maximum on the side;
+          // P stays in registers (64) until that is known to be at most 2^8 above, else
+          // O is rescaled and the weights are made again (the first tile of a piece
+          // always: its first maximum).  Scores 16 at a time, the next on their way.
+          uint32_t pk[BKV / 2];
+          float mx = -INFINITY, lt = 0.0f;
+          auto weigh = [&](float m) {
+            const float ms = m == -INFINITY ? 0.0f : m * p.scale_log2;
+            // two at a time (packed fp32 multiply-adds and sums)
+            const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), ms2 = pack_f32x2(-ms, -ms);
+            uint64_t ls4[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of zeros
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t sr[2][16];
+            tmem_ld_32x32b_x16(scol, sr[0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
-          tmem_ld_32x32b_x32(scol, sr[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(scol + ((c + 1) & 3) * 32, sr[(c + 1) & 1]);  // the last: the weights' first
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx8[(e >> 1) & 7] = fmaxf(fmaxf(mx8[(e >> 1) & 7], __uint_as_float(sr[c & 1][e])),
-                                        __uint_as_float(sr[c & 1][e + 1]));
-          }
-          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-          const float m_new = fmaxf(m_used, mx);
-          bool need = false;
-          if (m_used == -INFINITY)
-            m_used = m_new;  // O and l are still zero for this row
-          else
-            need = m_new > m_used + thresh;
-          if (!first && __any_sync(0xffffffffu, need)) {
-            // the stream's last P V came before this S, so it has landed
-            const float alpha = need ? ex2f((m_used - m_new) * p.scale_log2) : 1.0f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t rr[32];
-              tmem_ld_32x32b_x32(ocol + w * D + c * 32, rr);
+            for (int c = 0; c < BKV / 16; ++c) {
               tmem_wait_ld();
+              if (c + 1 < BKV / 16) tmem_ld_32x32b_x16(scol + (c + 1) * 16, sr[(c + 1) & 1]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
-              tmem_st_32x32b_x32(ocol + w * D + c * 32, rr);
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t s0 = sr[c & 1][2 * e], s1 = sr[c & 1][2 * e + 1];
+                mx4[e & 3] = fmaxf(fmaxf(mx4[e & 3], __uint_as_float(s0)), __uint_as_float(s1));
+                float a, b;
+                unpack_f32x2(fma_f32x2(pack_u32x2(s0, s1), sc2, ms2), a, b);
+                a = ex2f(a);
+                b = ex2f(b);
+                ls4[e & 3] = add_f32x2(ls4[e & 3], pack_f32x2(a, b));
+                pk[c * 8 + e] = Half<F16>::pack2(a, b);
+              }
             }
-            tmem_wait_st();
-            if (need) {
-              l *= alpha;
-              m_used = m_new;
-            }
-          }
-          const float ms = m_used == -INFINITY ? 0.0f : m_used * p.scale_log2;
-          // weights two at a time (packed fp32 multiply-adds and sums)
-          const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), ms2 = pack_f32x2(-ms, -ms);
-          uint64_t ls4[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of zeros
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // P of 32 keys takes 16 columns, all read by then
-            uint32_t pk[16];
-            tmem_wait_ld();
-            if (c < 3) tmem_ld_32x32b_x32(scol + (c + 1) * 32, sr[(c + 1) & 1]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a, b;
-              unpack_f32x2(fma_f32x2(pack_u32x2(sr[c & 1][2 * e], sr[c & 1][2 * e + 1]), sc2, ms2), a, b);
-              a = ex2f(a);
-              b = ex2f(b);
-              ls4[e & 3] = add_f32x2(ls4[e & 3], pack_f32x2(a, b));
-              pk[e] = Half<F16>::pack2(a, b);
-            }
-            tmem_st_32x32b_x16(scol + c * 16, pk);
-          }
-          {
+            mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             float a, b;
             unpack_f32x2(add_f32x2(add_f32x2(ls4[0], ls4[1]), add_f32x2(ls4[2], ls4[3])), a, b);
-            l += a + b;
+            lt = a + b;
+          };
+          if (first) {  // only the maximum is wanted of this pass
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < BKV / 32; ++c) {
+              uint32_t rr[32];
+              tmem_ld_32x32b_x32(scol + c * 32, rr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(rr[e]));
+            }
+            m_used = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          }
+#pragma unroll 1
+          for (;;) {
+            weigh(m_used);
+            // a row that has seen nothing yet (O and l are zero) takes any maximum
+            const bool need = mx > m_used + thresh || (m_used == -INFINITY && mx != -INFINITY);
+            if (!__any_sync(0xffffffffu, need)) break;
+            // the stream's last P V came before this S, so it has landed
+            const float alpha = need && m_used != -INFINITY ? ex2f((m_used - mx) * p.scale_log2) : 1.0f;
+            if (!first) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t rr[32];
+                tmem_ld_32x32b_x32(ocol + w * D + c * 32, rr);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+                tmem_st_32x32b_x32(ocol + w * D + c * 32, rr);
+              }
+              tmem_wait_st();
+            }
+            l *= alpha;
+            if (need) m_used = mx;
+          }
+          l += lt;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t q[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) q[e] = pk[c * 16 + e];
+            tmem_st_32x32b_x16(scol + c * 16, q);
           }
           tmem_wait_st();
         }

@@ -162,7 +162,7 @@ def lib():
             "nc_tree_mask": (i32, [vp, vp, i32, i32, vp]),
             "nc_tree_attention": (i32, [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, sz,
                                         vp]),
-            "nc_tree_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
+            "nc_tree_attention_workspace_bytes": (sz, [i32] * 7),
             "nc_tree_accept": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
             "nc_sample": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp]),
             "nc_distill_topk": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp]),
@@ -824,7 +824,7 @@ def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stre
          _arg(where, "out", out, dt, (B, N, H, D), dev))
     if B == 0:
         return
-    need = lib().nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, window)
+    need = lib().nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, T_max, window)
     wp = wn = 0
     if workspace is None and need and dev >= 0:
         with _allocate_on(stream):

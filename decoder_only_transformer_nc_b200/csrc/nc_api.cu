@@ -1102,11 +1102,11 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
   return tree_mask_launch(parents, mask, B, N, S(stream));
 }
 
-size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int window) {
+size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window) {
   if (B < 1 || B > 65535 || N < 1 || N > kTreeMaxNodes || H < 1 || H > 4096 || Hkv < 1 || H % Hkv != 0 ||
-      (D != 64 && D != 128))
+      (D != 64 && D != 128) || T_max < 1 || T_max > (1 << 22))
     return 0;
-  return tree_attention_bytes(B, N, H, Hkv, D, window);
+  return tree_attention_bytes(B, N, H, Hkv, D, T_max, window);
 }
 
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
@@ -1121,7 +1121,7 @@ nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint1
   if (q_row_stride < (int64_t)H * D || q_row_stride % 8) return NC_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace))
     return NC_ERR_ALIGNMENT;
-  const size_t need = tree_attention_bytes(B, N, H, Hkv, D, window);
+  const size_t need = tree_attention_bytes(B, N, H, Hkv, D, T_max, window);
   if (need > 0 && (!workspace || ws_bytes < need)) return NC_ERR_WORKSPACE;
   if (nc_status s = device_ok()) return s;
   return tree_attention_launch(q, q_row_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window,
@@ -1199,9 +1199,9 @@ TreeLayout tree_layout(const nc_config* c, int B, int N) {
   L.o = take(M * H * D * 2);
   L.h = take(M * 4 * C * 2);
   L.acc = take(M * (nqkv > 4 * C ? nqkv : 4 * C) * 4);
-  // every layer has one of the two windows
-  L.attn = take(std::max(tree_attention_bytes(B, N, c->n_head, c->n_kv_head, c->head_dim, 0),
-                         tree_attention_bytes(B, N, c->n_head, c->n_kv_head, c->head_dim, c->short_window)));
+  // every layer has one of the two windows; a session of fewer positions needs no more
+  L.attn = take(std::max(tree_attention_bytes(B, N, c->n_head, c->n_kv_head, c->head_dim, c->seq_len, 0),
+                         tree_attention_bytes(B, N, c->n_head, c->n_kv_head, c->head_dim, c->seq_len, c->short_window)));
   L.x0 = (c->extras & NC_EXTRA_RESID_LAMBDAS) ? take(M * C * 4) : 0;
   L.xmid = (c->extras & NC_EXTRA_BACKOUT) ? take(M * C * 4) : 0;
   L.total = off;

@@ -257,7 +257,7 @@ nc_status tree_attention_launch(const uint16_t* q, int64_t q_stride, const uint1
                                 int Hkv, int D, int T_max, int window, bool f16, void* workspace,
                                 uint32_t* dev_status, cudaStream_t stream);
 // Workspace bytes of tree_attention_launch (0: none is used).
-size_t tree_attention_bytes(int B, int N, int H, int Hkv, int D, int window);
+size_t tree_attention_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window);
 // The tcgen05 kernel of the same attention (nc_tree_tc.cu), for the sizes that fit it.
 bool tree_attention_tc_fits(int B, int N, int H, int Hkv, int window);
 size_t tree_attention_tc_bytes(int D);

@@ -624,13 +624,23 @@ nc_status tree_mask_launch(const int32_t* parents, uint32_t* mask, int B, int N,
   return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
 }
 
-// Rows of a kv group beyond which the tcgen05 kernel takes over.
-static bool use_tc(int B, int N, int H, int Hkv, int window) {
-  return N * (H / Hkv) > 32 && tree_attention_tc_fits(B, N, H, Hkv, window);
+// Which kernel: the tcgen05 one starts later (about 10 us for next to nothing,
+// this file's 7.5) and reads the keys faster, and a row tile costs it the same
+// whether 4 or 128 of its rows are there.  Measured, us, this file's / tcgen05, at
+// D = 128: 8 rows of the cache, 4 kv heads, 200 / 1000 / 4000 keys: 16 rows a kv
+// head 9.1 / 14.8, 14.0 / 17.0, 27.0 / 23.4; 64 rows 12.6 / 15.0, 18.7 / 17.3,
+// 41.6 / 23.9; 128 rows 14.8 / 15.7, 31.7 / 17.9, 73.4 / 25.3; 16 rows of the
+// cache, 12 kv heads, 32 rows: 19.3 / 24.3, 55.6 / 35.4, 180 / 80.  The lengths
+// are not known here; half of what the cache may hold stands for them.
+static bool use_tc(int B, int N, int H, int Hkv, int D, int T_max, int window) {
+  const int rows = N * (H / Hkv);
+  const int keys = window > 0 && window < T_max ? window : T_max;
+  return (rows > 32 || (rows > 16 && keys >= 1536) || keys >= 4096 * 128 / D) &&
+         tree_attention_tc_fits(B, N, H, Hkv, window);
 }
 
-size_t tree_attention_bytes(int B, int N, int H, int Hkv, int D, int window) {
-  return use_tc(B, N, H, Hkv, window) ? tree_attention_tc_bytes(D) : 0;
+size_t tree_attention_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window) {
+  return use_tc(B, N, H, Hkv, D, T_max, window) ? tree_attention_tc_bytes(D) : 0;
 }
 
 nc_status tree_attention_launch(const uint16_t* q, int64_t q_stride, const uint16_t* kv, const uint16_t* cache,
@@ -638,7 +648,7 @@ nc_status tree_attention_launch(const uint16_t* q, int64_t q_stride, const uint1
                                 int Hkv, int D, int T_max, int window, bool f16, void* workspace,
                                 uint32_t* dev_status, cudaStream_t stream) {
   if (B == 0) return NC_OK;
-  if (use_tc(B, N, H, Hkv, window))
+  if (use_tc(B, N, H, Hkv, D, T_max, window))
     return tree_attention_tc_launch(q, q_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window, f16,
                                     workspace, dev_status, stream);
   const TreeAttnParams p{q, q_stride, kv, cache, lens, mask, out, N, H, Hkv, T_max, window,

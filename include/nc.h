@@ -638,7 +638,7 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * least nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where
  * that is 0); calls that overlap in time need one each.  The result is the same
  * run to run. */
-size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int window);
+size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window);
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
                             const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
                             int D, int T_max, int window, nc_dtype dtype, void* workspace, size_t ws_bytes,

@@ -161,7 +161,7 @@ def lib():
             "nc_accept_tree": (i32, [cfgp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, i32, vp, sz, vp]),
             "nc_tree_mask": (i32, [vp, vp, i32, i32, vp]),
             "nc_tree_attention": (i32, [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, sz,
-                                        vp]),
+                                        vp, vp]),
             "nc_tree_attention_workspace_bytes": (sz, [i32] * 7),
             "nc_tree_accept": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
             "nc_sample": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp]),
@@ -350,6 +350,7 @@ class Session:
         self.buffer = torch.empty(n, dtype=torch.uint8, device=device)
         self.pos = 0
         self._graph = None
+        self._filled = False  # prefill lays out the weights
         self._lens = self._tree = self._tree_ws = None
 
     def prefill(self, tokens, want_logits=False, stream=None):
@@ -363,7 +364,7 @@ class Session:
         _check(lib().nc_prefill(ctypes.byref(cfg), ctypes.byref(self.model.weights), _ptr(tokens), B, T,
                                 _ptr(logits), _ptr(self.buffer), self.buffer.numel(), self.T_max, _ptr(ws),
                                 ws.numel(), _stream(stream)), "nc_prefill")
-        self.pos = T
+        self.pos, self._filled = T, True
         self._lens = self._tree = None
         return logits
 
@@ -386,6 +387,14 @@ class Session:
             raise NcError(1, f"{where}: the rows have lengths of their own after accept_tree (decode_tree goes on)")
         self._tree = None
 
+    def _used_on(self, stream, *tensors):
+        """The session's own tensors may be dropped while a call on another stream than
+        the one they were made on still runs."""
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream(self.buffer.device)
+        for t in tensors:
+            t.record_stream(s)
+
     @property
     def lens(self):
         """Committed positions of every row: int32 CUDA tensor [B]."""
@@ -400,11 +409,16 @@ class Session:
         tokens, parents: int32 [B, N], N <= 128; parents[b, i] < i is node i's
         parent, -1 for a root, -2 for an unused node.  Node 0 is the row's next
         token.  ``accept_tree`` then moves the path that the samples confirm
-        into the cache; without it the tree is dropped."""
+        into the cache (tokens and parents stay as they are until then); without
+        it the tree is dropped.  To capture steps in a graph that is replayed, use
+        nc_decode_tree and nc_accept_tree with buffers of your own: the lengths a
+        captured call of this method read are those of its capture."""
         import torch
         cfg, device = self.model.cfg, self.buffer.device
         dev = self.buffer.get_device()
         where = "Session.decode_tree"
+        if not self._filled:
+            raise NcError(1, f"{where}: no prefill before it (one of no tokens will do)")
         if tokens.dim() != 2 or tokens.shape[0] != self.B:
             raise NcError(3, f"{where}: tokens {tuple(tokens.shape)}, rows {self.B}")
         N = tokens.shape[1]
@@ -421,6 +435,7 @@ class Session:
                 logits = torch.empty((self.B, N, cfg.vocab), dtype=torch.float32, device=device)
         lp = _arg(where, "logits", logits, torch.float32, (self.B, N, cfg.vocab), dev)
         self._tree = None
+        self._used_on(stream, lens, self._tree_ws)
         _launch(where, dev, stream, lib().nc_decode_tree, ctypes.byref(cfg), ctypes.byref(self.model.weights), tp, pp,
                 lens.data_ptr(), self.B, N, lp, self.buffer.data_ptr(), self.buffer.numel(), self.T_max,
                 self._tree_ws.data_ptr(), self._tree_ws.numel())
@@ -443,6 +458,7 @@ class Session:
         with _allocate_on(stream):
             path = torch.empty((self.B, N), dtype=torch.int32, device=device)
             count, nxt, lens_out = (torch.empty(self.B, dtype=torch.int32, device=device) for _ in range(3))
+        self._used_on(stream, lens, self._tree_ws)
         _launch(where, dev, stream, lib().nc_accept_tree, ctypes.byref(self.model.cfg), tokens.data_ptr(),
                 parents.data_ptr(), sp, lens.data_ptr(), self.B, N, path.data_ptr(), count.data_ptr(), nxt.data_ptr(),
                 lens_out.data_ptr(), self.buffer.data_ptr(), self.buffer.numel(), self.T_max,
@@ -752,6 +768,18 @@ def _arg(where, name, t, dtype, shape, dev):
     raise NcError(1, f"{where}: {name} is on {t.device}, the first tensor is on another device")
 
 
+def _status_word(where, t, dev):
+    """Address of a device status word: 4 aligned bytes or more of any type (0 for None)."""
+    if t is None:
+        return 0
+    p = _arg(where, "status", t, t.dtype, t.shape, dev)
+    if t.numel() * t.element_size() < 4:
+        raise NcError(5, f"{where}: status has {t.numel() * t.element_size()} bytes, 4 are needed")
+    if p % 4:
+        raise NcError(4, f"{where}: status is not aligned to 4 bytes")
+    return p
+
+
 def _launch(where, dev, stream, fn, *args):
     """Calls a library function on device ``dev`` (an index), on ``stream`` (of
     that device) or the device's current stream."""
@@ -795,17 +823,19 @@ def tree_mask(parents, mask, stream=None):
     dev = parents.get_device()
     a = (_arg(where, "parents", parents, torch.int32, (B, N), dev),
          _arg(where, "mask", mask, torch.int32, (B, N, (N + 31) // 32), dev))
-    _launch(where, dev, stream, lib().nc_tree_mask, *a, B, N)
+    if B:
+        _launch(where, dev, stream, lib().nc_tree_mask, *a, B, N)
 
 
-def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stream=None):
+def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, status=None, stream=None):
     """Attention of the drafted nodes of every row over the cache and their
     ancestors (nc_tree_attention).
 
     q [B, N, H, D] (the nodes may be strided), kv [B, N, 2, Hkv, D], cache
     [B, T_max, 2, Hkv, D], out [B, N, H, D]: fp16 or bf16; lens [B] int32, mask
     [B, N, ceil(N / 32)] int32 (tree_mask).  workspace: a uint8 tensor of
-    nc_tree_attention_workspace_bytes bytes (None: a new one)."""
+    nc_tree_attention_workspace_bytes bytes (None: a new one).  status: a device
+    status word (int32 or uint8 tensor) or None."""
     import torch
     where = "tree_attention"
     if q.dim() != 4 or cache.dim() != 5:
@@ -833,7 +863,7 @@ def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stre
         wn = workspace.numel()
         wp = _arg(where, "workspace", workspace, torch.uint8, (wn,), dev)
     _launch(where, dev, stream, lib().nc_tree_attention, q.data_ptr(), qs, *a, B, N, H, Hkv, D, T_max, window, _dt(q),
-            wp, wn)
+            wp, wn, _status_word(where, status, dev))
 
 
 def sample(logits, u, tokens, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
@@ -913,4 +943,4 @@ def distill_topk(z, teacher_idx, teacher_logits, token_loss, dz=None, tau=1.0, c
         dzp = _arg(where, "dz", dz, dz.dtype, (M, V), dev)
     if M:
         _launch(where, dev, stream, lib().nc_distill_topk, *a, dzp, kind, M, V, K, tau, cap,
-                _arg(where, "status", status, None if status is None else status.dtype, None if status is None else status.shape, dev))
+                _status_word(where, status, dev))

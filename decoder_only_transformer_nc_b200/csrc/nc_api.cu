@@ -1112,7 +1112,7 @@ size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, in
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
                             const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
                             int D, int T_max, int window, nc_dtype dtype, void* workspace, size_t ws_bytes,
-                            void* stream) {
+                            uint32_t* dev_status, void* stream) {
   if (!q || !kv || !cache || !lens || !mask || !out || B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || !dtype_ok(dtype))
     return NC_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || N < 1 || N > kTreeMaxNodes || T_max < 1 || T_max > (1 << 22) ||
@@ -1125,7 +1125,7 @@ nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint1
   if (need > 0 && (!workspace || ws_bytes < need)) return NC_ERR_WORKSPACE;
   if (nc_status s = device_ok()) return s;
   return tree_attention_launch(q, q_row_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window,
-                               dtype == NC_F16, workspace, nullptr, S(stream));
+                               dtype == NC_F16, workspace, dev_status, S(stream));
 }
 
 nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const uint32_t* mask, const int32_t* sampled,
@@ -1157,11 +1157,13 @@ nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, con
 nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const float* teacher_logits,
                           const float* row_weight, float* token_loss, void* dz, nc_grad_dtype dz_dtype, int M, int V,
                           int K, float tau, float cap, uint32_t* dev_status, void* stream) {
-  if (!z || !teacher_idx || !teacher_logits || !token_loss || M < 0 || !(tau > 0.0f) || !std::isfinite(tau) ||
-      !(cap >= 0.0f) || !std::isfinite(cap) || (int)dz_dtype < NC_GRAD_BF16 || (int)dz_dtype > NC_GRAD_NONE ||
+  // the coefficients of tanh hold cap^-6, and the logits' scale cap / tau: both in fp32
+  auto scale_ok = [](float x) { return x >= 1.0f / 65536 && x <= 65536.0f; };
+  if (!z || !teacher_idx || !teacher_logits || !token_loss || M < 0 || !scale_ok(tau) ||
+      !(cap == 0.0f || scale_ok(cap)) || (int)dz_dtype < NC_GRAD_BF16 || (int)dz_dtype > NC_GRAD_NONE ||
       (dz == nullptr) != (dz_dtype == NC_GRAD_NONE) || dz == z)
     return NC_ERR_INVALID_ARG;
-  if (V < 1 || K < 1 || K > 1024) return NC_ERR_SHAPE;
+  if (V < 1 || V > (1 << 24) || K < 1 || K > 1024) return NC_ERR_SHAPE;
   if (nc_status s = device_ok()) return s;
   const int kind = dz_dtype == NC_GRAD_NONE ? 0 : dz_dtype == NC_GRAD_F32 ? 1 : dz_dtype == NC_GRAD_BF16 ? 2 : 3;
   return distill_topk_launch(z, teacher_idx, teacher_logits, row_weight, token_loss, dz, kind, M, V, K, tau, cap,

@@ -633,16 +633,18 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * (q_row_stride >= H D, a multiple of 8); kv [B, N, 2, Hkv, D]; cache
  * [B, T_max, 2, Hkv, D]; out [B, N, H, D]; 16-bit in format dtype.  lens [B] is
  * clamped to [0, T_max]; positions at and past it are not read.  D in {64,
- * 128}, 1 <= N <= 128, 1 <= T_max <= 2^22, B <= 65535, H <= 4096.  K and V of committed positions
- * inside the root's window and of used nodes must be finite.  workspace: at
- * least nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where
- * that is 0); calls that overlap in time need one each.  The result is the same
- * run to run. */
+ * 128}, 1 <= N <= 128, 1 <= T_max <= 2^22, B <= 65535, H <= 4096.  Bits of mask
+ * at and past N are 0.  K and V of committed positions inside the root's window
+ * and of used nodes must be finite.  workspace: at least
+ * nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where that is
+ * 0); calls that overlap in time need one each.  dev_status (or NULL) gets
+ * NC_DEV_TIMEOUT if a pipeline wait ran out (out is not valid then).  The result
+ * is the same run to run. */
 size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window);
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
                             const int32_t* lens, const uint32_t* mask, uint16_t* out, int B, int N, int H, int Hkv,
                             int D, int T_max, int window, nc_dtype dtype, void* workspace, size_t ws_bytes,
-                            void* stream);
+                            uint32_t* dev_status, void* stream);
 
 /* The accepted path of each row's tree, and its K/V moved into the cache: the
  * path starts at node 0 (if it is used) and goes on from node a to its first
@@ -673,9 +675,13 @@ nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const ui
  * off; top_p <= 0 (or NaN) and min_p >= 1 keep the largest logits only.  u is
  * clamped to [0, 1] (NaN: 0); 1 takes the last kept token.  NaN logits count as
  * -inf, which is never sampled; a row of those alone gives token -1 and logprob
- * -inf.  logprob may be NULL.  Weights are exact to 2^-47 or better at V <=
- * 32768 (an absolute unit of V / 2^62; smaller weights count as 0) and sums are
- * exact, so the result is the same run to run.  1 <= V <= 2^24. */
+ * -inf.  The largest logit weighs 1 also where it is +inf.  logprob may be NULL.
+ * The token is that of weights rounded to an absolute unit of V / 2^62 (2^-47 at
+ * V <= 32768; smaller ones count as 0) and exact sums, the same run to run.
+ * logprob may come from fp32 weights: the mass in it is within 3e-7 + 4.5e-8
+ * |log2 w| of each weight, relative (a few 1e-8 in practice).  A row whose copy to
+ * the SM does not arrive in time gives token -1 and logprob NaN.
+ * 1 <= V <= 2^24. */
 nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, const float* temperature,
                     const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, float* logprob,
                     int M, int V, void* stream);
@@ -695,9 +701,12 @@ typedef enum { NC_GRAD_BF16 = 0, NC_GRAD_F16 = 1, NC_GRAD_F32 = 2, NC_GRAD_NONE 
  * fp32, dz [M, V] in dz_dtype or NULL (with NC_GRAD_NONE).  An entry with index
  * -1 or logit -inf is unused; an index outside [-1, V) is unused and sets
  * NC_DEV_TARGET_RANGE; an index may occur more than once.  A row with no entry
- * has loss 0 and gradient 0.  fp16 gradients saturate at +-65504.  tau > 0,
- * cap >= 0, 1 <= K <= 1024, 1 <= V.  z needs a finite maximum in each row.  dz
- * may not overlap z.  Same result run to run. */
+ * has loss 0 and gradient 0.  fp16 gradients saturate at +-65504.  2^-16 <= tau
+ * <= 2^16, cap 0 or in the same range, 1 <= K <= 1024, 1 <= V <= 2^24.  z needs a
+ * finite maximum in each row, teacher logits are finite or -inf.  dz may not
+ * overlap z.  dev_status (or NULL) also gets NC_DEV_TIMEOUT if the parts of a row
+ * did not meet in time (its outputs are not written then).  Same result run to
+ * run. */
 nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const float* teacher_logits,
                           const float* row_weight, float* token_loss, void* dz, nc_grad_dtype dz_dtype, int M, int V,
                           int K, float tau, float cap, uint32_t* dev_status, void* stream);

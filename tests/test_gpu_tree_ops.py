@@ -142,6 +142,92 @@ def test_tree_attention_reads_nothing_unseen(gpu, dt, H, W):
     _check_attn(out, clean[2], clean[0], clean[1], lens, mask, W, dt)
 
 
+def test_tree_attention_many_rows_strided_q_and_own_workspace(gpu):
+    """More rows of the cache than the tensor-core kernel plans for (trees of a size that it takes else);
+    the q columns of a packed projection, and a workspace of the caller's, one too small refused."""
+    B, N, H, Hkv, D, T = 1030, 40, 1, 1, 64, 24
+    lens = [(7 * b) % 25 for b in range(B)]
+    q, kv, cache, lens, mask = _attn_case(8, B, N, H, Hkv, D, T, lens, "fp16", "ragged")
+    out = torch.full_like(q, 7.0).to(DEV)
+    assert gpu.lib().nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, T, 0) == 0
+    gpu.tree_attention(q.to(DEV), kv.to(DEV), cache.to(DEV), _dev(lens), _mask_i32(mask), out)
+    _check_attn(out, q, kv, cache, lens, mask, 0, "fp16")
+    B, N, H, Hkv, D, T = 3, 50, 6, 2, 128, 700
+    q, kv, cache, lens, mask = _attn_case(9, B, N, H, Hkv, D, T, [700, 1, 300], "bf16", "random")
+    need = gpu.lib().nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, T, 0)
+    assert need > 0
+    packed = torch.full((B, N, (H + 2 * Hkv) * D), math.nan, dtype=DT["bf16"])
+    packed[:, :, :H * D] = q.reshape(B, N, H * D)
+    qs = packed.to(DEV)[:, :, :H * D].view(B, N, H, D)
+    args = (qs, kv.to(DEV), cache.to(DEV), _dev(lens), _mask_i32(mask))
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.empty((B, N, H, D), dtype=DT["bf16"], device=DEV)
+    for w in (ws[:need - 1], ws[:0]):
+        with pytest.raises(gpu.NcError) as e:
+            gpu.tree_attention(*args, out, workspace=w)
+        assert e.value.code == 5
+    gpu.tree_attention(*args, out, workspace=ws[:need], status=st)
+    _check_attn(out, q, kv, cache, lens, mask, 0, "bf16")
+    assert (ws[need:] == 255).all() and int(st) == 0
+
+
+@pytest.mark.parametrize("N", [5, 64])  # each of the kernels
+def test_offsets_past_32_bits(gpu, N):
+    """A cache of 2^31 elements a row: the last positions of three rows under a window, the accepted K/V
+    there, and logits rows 2^31 elements apart."""
+    B, H, Hkv, D, T, W = 3, 8, 8, 128, 1 << 20, 200
+    lens = [T - 130, T - 200, 1000]
+    q, kv, near, _, mask = _attn_case(2, B, N, H, Hkv, D, 300, [0] * B, "bf16", "random")
+    cache = torch.empty((1, B, T, 2, Hkv, D), dtype=DT["bf16"], device=DEV)
+    for b in range(B):
+        cache[0, b, lens[b] - 300:lens[b]] = near[b].to(DEV)
+    out = torch.empty((B, N, H, D), dtype=DT["bf16"], device=DEV)
+    words = _mask_i32(mask)
+    gpu.tree_attention(q.to(DEV), kv.to(DEV), cache[0], _dev(np.array(lens, np.int32)), words, out, W)
+    _check_attn(out, q, kv, near, np.array([300] * B), mask, W, "bf16")
+    par = np.full((B, N), -1, np.int32)
+    par[:, 1:] = np.arange(N - 1)
+    words = _mask_i32(o64.tree_mask(par))
+    tok = torch.arange(B * N, dtype=torch.int32, device=DEV).view(B, N)
+    path, (count, nxt, lo) = torch.empty_like(tok), torch.empty((3, B), dtype=torch.int32, device=DEV)
+    gpu.tree_accept(tok, _dev(par), words, tok + 1, _dev(np.array(lens, np.int32)), kv.to(DEV)[None], cache, path, count,
+                    nxt, lo)
+    assert count.tolist() == [N] * B
+    for b in range(B):
+        assert torch.equal(cache[0, b, lens[b]:lens[b] + N], kv[b].to(DEV))
+        assert torch.equal(cache[0, b, lens[b] - 300:lens[b]], near[b].to(DEV))
+    del cache
+    V, ld = 5000, 1 << 31
+    x = torch.empty(ld + V, device=DEV).as_strided((2, V), (ld, 1))
+    x.copy_(3 * torch.randn((2, V), device=DEV))
+    u, a, b = torch.rand(2, device=DEV), *torch.empty((2, 2), dtype=torch.int32, device=DEV)
+    gpu.sample(x, u, a)
+    gpu.sample(x.contiguous(), u, b)
+    assert torch.equal(a, b)
+
+
+def test_tree_attention_calls_side_by_side(gpu):
+    """The same and another problem on four streams at once, each call with its own workspace."""
+    cases = [(4, 64, 4, 2, 128, 500, [500, 7, 256, 0]), (2, 33, 8, 2, 128, 900, [900, 640])]
+    ins, want = [], []
+    for i, (B, N, H, Hkv, D, T, lens) in enumerate(cases):
+        q, kv, cache, lens, mask = _attn_case(30 + i, B, N, H, Hkv, D, T, lens, "bf16", "random")
+        a = [q.to(DEV), kv.to(DEV), cache.to(DEV), _dev(lens), _mask_i32(mask)]
+        out = torch.empty_like(a[0])
+        gpu.tree_attention(*a, out)
+        ins.append(a)
+        want.append(out)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = [[torch.empty_like(ins[k % 2][0]) for k in range(4)] for _ in range(6)]
+    for turn in outs:
+        for k, s in enumerate(streams):
+            gpu.tree_attention(*ins[k % 2], turn[k], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[k % 2]) for turn in outs for k, o in enumerate(turn))
+
+
 # ------------------------------------------------------------------ acceptance
 
 @pytest.mark.parametrize("B,N,L,Hkv,D,T", [(1, 1, 1, 1, 64, 3), (3, 8, 4, 2, 64, 20), (5, 33, 2, 1, 128, 40),
@@ -336,6 +422,72 @@ def test_distill(gpu, M, V, K, dz, cap, tau):
     dzt = {"fp32": torch.float32, "none": None, **DT}[dz]
     _, _, st = _check_distill(gpu, z, idx, t, tau, cap, w, dzt)
     assert int(st[0]) == 0
+
+
+@pytest.mark.parametrize("V", [65536, 65537, 70001, 140000])  # the last that fits registers, and beyond
+@pytest.mark.parametrize("dz,cap", [("fp32", 15.0), ("bf16", 0.0), ("fp16", 15.0), ("none", 15.0)])
+def test_distill_long_rows(gpu, V, dz, cap):
+    rng = np.random.default_rng(V)
+    M, K = 3, 40
+    z = (3 * rng.standard_normal((M, V))).astype(np.float32)
+    idx = rng.integers(0, V, (M, K)).astype(np.int32)
+    idx[0, 1], idx[0, 2], idx[1, 5:] = idx[0, 0], -1, -1
+    idx[2] = -1
+    idx[0, 3], idx[0, 4] = 0, V - 1
+    t = (2 * rng.standard_normal((M, K))).astype(np.float32)
+    _check_distill(gpu, z, idx, t, 1.0, cap, rng.random(M).astype(np.float32), {"fp32": torch.float32, "none": None, **DT}[dz])
+
+
+@pytest.mark.parametrize("cap,tau", [(2.0 ** -16, 2.0 ** -12), (0.3, 1.0), (300.0, 30.0), (65536.0, 65536.0)])
+def test_distill_caps_of_any_size(gpu, cap, tau):
+    rng = np.random.default_rng(4)
+    M, V, K = 3, 5000, 20
+    z = (cap * rng.standard_normal((M, V)) * np.array([[0.1], [1.0], [4.0]])).astype(np.float32)
+    idx = np.stack([rng.permutation(V)[:K] for _ in range(M)]).astype(np.int32)
+    t = (tau * rng.standard_normal((M, K))).astype(np.float32)
+    _check_distill(gpu, z, idx, t, tau, cap, None, torch.float32)
+
+
+@pytest.mark.parametrize("dz", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,zo,do", [(33, 1, 0), (4099, 3, 1), (8192, 1, 1), (8192, 2, 3), (32768, 0, 1), (70001, 1, 2)])
+def test_distill_at_any_alignment(gpu, V, zo, do, dz):
+    """z and dz that start anywhere: equal to the aligned call to the order of the sums, and nothing
+    beside dz is written."""
+    dzt = {"fp32": torch.float32, **DT}[dz]
+    M, K = 5, 16
+    z = 3 * torch.randn((M, V), device=DEV)
+    idx = torch.randint(0, V, (M, K), dtype=torch.int32, device=DEV)
+    t = torch.randn((M, K), device=DEV)
+    zb = torch.full((M * V + 8,), math.nan, device=DEV)
+    zb[zo:zo + M * V] = z.flatten()
+    db = torch.full((M * V + 8,), 7.0, dtype=dzt, device=DEV)
+    la, lb, da = torch.empty(M, device=DEV), torch.empty(M, device=DEV), torch.empty((M, V), dtype=dzt, device=DEV)
+    gpu.distill_topk(z, idx, t, la, da, tau=0.7)
+    gpu.distill_topk(zb[zo:zo + M * V].view(M, V), idx, t, lb, db[do:do + M * V].view(M, V), tau=0.7)
+    # sums of p in another order: V / 4096 + 20 additions of at most half a step each a side
+    rel = 2.0 ** -24 * 2 * (V / 4096 + 20) + 2.0 ** -24 * 16 * 15 / 0.7
+    assert (la - lb).abs().max().item() <= 0.49 * 2 * rel + 2.0 ** -22 * la.abs().max().item()
+    got, want = db[do:do + M * V].view(M, V).double(), da.double()
+    tiny = torch.finfo(dzt).smallest_normal * torch.finfo(dzt).eps
+    # 0.7 p (1 - t^2) of an entry is at most 0.7, and p - q of a teacher's entry cancels
+    assert ((got - want).abs() <= torch.finfo(dzt).eps * want.abs() + rel * (want.abs() + 0.7) * 2 + tiny).all()
+    assert (db[:do] == 7).all() and (db[do + M * V:] == 7).all()
+
+
+def test_distill_many_rows(gpu):
+    """More rows than one launch takes; the rows around the border against the definition."""
+    M, V, K = 65535 + 9, 70, 4
+    rng = np.random.default_rng(6)
+    z = (3 * rng.standard_normal((M, V))).astype(np.float32)
+    idx = rng.integers(-1, V, (M, K)).astype(np.int32)
+    t = rng.standard_normal((M, K)).astype(np.float32)
+    w = rng.random(M).astype(np.float32)
+    loss, dz = torch.full((M,), math.nan, device=DEV), torch.full((M, V), math.nan, device=DEV)
+    gpu.distill_topk(_dev(z), _dev(idx), _dev(t), loss, dz, tau=1.0, cap=15.0, row_weight=_dev(w))
+    assert not loss.isnan().any() and not dz.isnan().any()
+    s = slice(65535 - 6, None)
+    a, b, _ = _check_distill(gpu, z[s], idx[s], t[s], 1.0, 15.0, w[s], torch.float32)
+    assert (a - loss[s]).abs().max().item() <= 1e-5 and (b - dz[s]).abs().max().item() <= 1e-5
 
 
 def test_distill_repeated_missing_and_bad_entries(gpu):

@@ -134,6 +134,38 @@ def test_tree_of_one_is_a_decode_step(gpu):
         assert count.tolist() == [1] * B
 
 
+def test_trees_from_an_empty_text_and_refusals(gpu):
+    """The first tokens of a text by trees; what decode_tree and accept_tree need before them; calls
+    on other streams than the one that made the session's tensors."""
+    s, B = SHAPES["tiny"], 2
+    w, ex, model = _model(gpu, s, False)
+    x, _ = make_tokens(s, batch=B, seed=21)
+    parents = np.array([[-1, 0, 1]] * B, np.int32)
+    sess = gpu.Session(model, B, 40)
+    tok, par = _dev(x[:, :3]), _dev(parents)
+    with pytest.raises(gpu.NcError):
+        sess.decode_tree(tok, par)
+    sess.prefill(torch.empty((B, 0), dtype=torch.int32, device=DEV))
+    with pytest.raises(gpu.NcError):
+        sess.accept_tree(tok)
+    text = [[] for _ in range(B)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(6):
+        tok = _dev(x[:, 3 * k:3 * k + 3])
+        sampled = _dev(np.stack([x[:, 3 * k + 1], x[:, 3 * k + 2], x[:, 3 * k + 3]], 1))
+        torch.cuda.synchronize()
+        logits = sess.decode_tree(tok, par, stream=streams[k % 2])
+        torch.cuda.synchronize()
+        _check_nodes(s, w, ex, text, x[:, 3 * k:3 * k + 3], parents, logits)
+        _, count, nxt = sess.accept_tree(sampled, stream=streams[(k + 1) % 2])
+        torch.cuda.synchronize()
+        assert count.tolist() == [3] * B and nxt.tolist() == x[:, 3 * k + 3].tolist()
+        text = [t + [int(v) for v in x[b, 3 * k:3 * k + 3]] for b, t in enumerate(text)]
+    assert sess.lens.tolist() == [18] * B
+    with pytest.raises(gpu.NcError):
+        sess.decode(_dev(x[:, 18]))
+
+
 def test_sampled_generation_in_one_graph(gpu):
     """decode_tree, sample and acceptance captured together (the entry points on preallocated
     buffers) and replayed until the cache is full: at every step the logits are the oracle's for

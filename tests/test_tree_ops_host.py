@@ -32,7 +32,7 @@ A = 1 << 40  # an aligned address that no check dereferences
 
 def _c_attn(nc, q=A, qs=512, kv=A, cache=A, lens=A, mask=A, out=A, B=1, N=4, H=4, Hkv=2, D=128, T=64, win=0, dt=1, ws=None,
             wn=0):
-    return nc.lib().nc_tree_attention(q, qs, kv, cache, lens, mask, out, B, N, H, Hkv, D, T, win, dt, ws, wn, None)
+    return nc.lib().nc_tree_attention(q, qs, kv, cache, lens, mask, out, B, N, H, Hkv, D, T, win, dt, ws, wn, None, None)
 
 
 def test_tree_attention_refusals(nclib):
@@ -102,7 +102,9 @@ def test_distill_refusals(nclib):
 
     for bad, want in [(dict(z=None), 1), (dict(loss=None), 1), (dict(dz=None), 1), (dict(dt=3), 1), (dict(dt=4), 1),
                       (dict(dz=A), 1), (dict(tau=0.0), 1), (dict(tau=math.inf), 1), (dict(tau=math.nan), 1),
-                      (dict(cap=-1.0), 1), (dict(cap=math.nan), 1), (dict(K=0), 3), (dict(K=1025), 3), (dict(V=0), 3)]:
+                      (dict(cap=-1.0), 1), (dict(cap=math.nan), 1), (dict(K=0), 3), (dict(K=1025), 3), (dict(V=0), 3),
+                      (dict(V=(1 << 24) + 1), 3), (dict(tau=1e-5), 1), (dict(tau=1e5), 1), (dict(cap=1e-5), 1),
+                      (dict(cap=1e5), 1)]:
         assert dis(**bad) == want, bad
     b = dict(z=_f(2, 10), teacher_idx=_i(2, 3), teacher_logits=_f(2, 3), token_loss=_f(2), dz=_f(2, 10))
     assert _code(nclib, nclib.distill_topk, **b) == 8
@@ -111,6 +113,25 @@ def test_distill_refusals(nclib):
         assert _code(nclib, nclib.distill_topk, **{**b, name: t}) == want, name
     with pytest.raises(TypeError):
         nclib.distill_topk(**{**b, "dz": _i(2, 10)})
+
+
+def test_status_words_and_empty_batches(nclib):
+    a = dict(q=_h(2, 3, 4, 64), kv=_h(2, 3, 2, 2, 64), cache=_h(2, 9, 2, 2, 64), lens=_i(2), mask=_i(2, 3, 1),
+             out=_h(2, 3, 4, 64))
+    d = dict(z=_f(2, 10), teacher_idx=_i(2, 3), teacher_logits=_f(2, 3), token_loss=_f(2), dz=_f(2, 10))
+    byte = torch.zeros(16, dtype=torch.uint8)
+    byte = byte[-byte.data_ptr() % 4:]
+    for fn, args in [(nclib.tree_attention, a), (nclib.distill_topk, d)]:
+        # a wrong word is found before the call, a right one gets as far as the missing device
+        for t, want in [(byte[:3], 5), (byte[1:9], 4), (_i(4)[::2], 1), (byte[:4], 8), (_i(1), 8)]:
+            assert _code(nclib, fn, **args, status=t) == want, (fn.__name__, t.shape)
+    # no rows: nothing is done
+    nclib.tree_mask(_i(0, 5), _i(0, 5, 1))
+    nclib.tree_attention(_h(0, 3, 4, 64), _h(0, 3, 2, 2, 64), _h(0, 9, 2, 2, 64), _i(0), _i(0, 3, 1), _h(0, 3, 4, 64))
+    nclib.sample(_f(0, 10), _f(0), _i(0))
+    nclib.distill_topk(_f(0, 10), _i(0, 3), _f(0, 3), _f(0))
+    nclib.tree_accept(_i(0, 3), _i(0, 3), _i(0, 3, 1), _i(0, 3), _i(0), _h(2, 0, 3, 2, 1, 64), _h(2, 0, 9, 2, 1, 64),
+                      _i(0, 3), _i(0), _i(0), _i(0))
 
 
 def test_tree_workspace_and_step_refusals(nclib):

@@ -78,17 +78,30 @@ __device__ __forceinline__ double wide(float x) {
   return __hiloint2double(((u >> 3) & (int)0x8fffffffu) + (896 << 20), u << 29);
 }
 
-// A sum of fp32 values in [0, 1] (a little more for rounding) in two fp32 parts:
-// what an addition rounds off is kept.  It starts at 2, so the sum is never the
-// smaller one, which makes the rounded-off part exact in two operations.
+// A sum of weights (at most 1, a little more for rounding) in two fp32 parts: what
+// an addition rounds off is kept.  It starts at 8, so the sum is never the smaller
+// one, which makes the rounded-off part exact in two operations.  Four weights are
+// added up first, unless one may be the maximum's: what is beside a 1 counts in
+// full (the logprob of a token that is nearly certain).
 struct Sum2 {
-  float hi = 2.0f, lo = 0.0f;
+  float hi = 8.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float a, float b, float c, float d) {
+    const float x = (a + b) + (c + d);
+    if (x < 1.0f) {
+      add(x);
+    } else {
+      add(a);
+      add(b);
+      add(c);
+      add(d);
+    }
+  }
   __device__ __forceinline__ void add(float x) {
     const float t = hi + x;
     lo += x - (t - hi);
     hi = t;
   }
-  __device__ __forceinline__ double value() const { return ((double)hi - 2.0) + (double)lo; }
+  __device__ __forceinline__ double value() const { return ((double)hi - 8.0) + (double)lo; }
 };
 
 // A row's exponential: exp((l - mx) / T) in units of 2^-sh, rounded to nearest.
@@ -131,31 +144,39 @@ struct Expo {
   __device__ __forceinline__ int64_t operator()(float l) const { return raw(l) - kRaw0; }
 };
 
-// The same as an fp32 number (1 for the maximum): y = n + f, the remainder f from
-// the unrounded product, 2^f by the hardware, n into the exponent.
+// The same as an fp32 number (1 for the maximum).  l log2(e) / T = n + f, the
+// remainder f from the unrounded product; less the maximum's own n and f (phi)
+// it is y without the rounding of l - mx, which for far tokens is an error in
+// proportion to |y|.  2^(f - phi) by the hardware, n into the exponent.
 struct Expo32 {
-  float mx, least, c_hi, c_lo;
-  // Relative error of a weight: 2^-22 (2^f), 2^-24 ln 2 (f), and 2^-24 |y| ln 2 (the
-  // difference l - mx).
-  static constexpr double kErr = 3e-7, kErrY = 4.5e-8;
-  static constexpr double kHist = 2e-6;  // the two for |y| < 31: a sum of weights from 2^-30 on
+  float least, c_hi, c_lo, m0, phi;
+  // Relative error of a weight: 2^-22 (2^f) and ln 2 times that of f - phi, at most 4
+  // roundings of 2^-25; and of a sum of four, two roundings.
+  static constexpr double kErr = 4.5e-7;
+  static constexpr float kMagic = 12582912.0f;  // 1.5 2^23: the nearest integer in the low bits
 
-  __device__ Expo32(float mx_, double c, float T) : mx(mx_) {
+  __device__ Expo32(float mx, double c, float T) {
     c_hi = (float)c;
     c_lo = (float)(c - (double)c_hi);
-    least = mx_ - 69.3f * T;  // below it a weight is 2^-100: nothing beside 1
+    least = mx - 69.3f * T;  // below it a weight is 2^-100: nothing beside 1
+    m0 = 2.0f * kMagic - fmaf(mx, c_hi, kMagic);
+    const float t = fmaf(mx, c_hi, m0);
+    phi = (t - kMagic) + fmaf(mx, c_lo, fmaf(mx, c_hi, m0 - t));
   }
   __device__ static bool usable(float mx, float T) {
     return T > 1e-20f && T < 1e20f && fabsf(mx) < 1e5f * T;
   }
-  // d: l - mx
-  __device__ __forceinline__ float operator()(float l, float& d) const {
-    d = fmaxf(l, least) - mx;  // also -inf and NaN
-    constexpr float kMagic = 12582912.0f;  // 1.5 2^23: the nearest integer in the low bits
-    const float t = fmaf(d, c_hi, kMagic);
+  __device__ __forceinline__ float operator()(float l) const {
+    l = fmaxf(l, least);  // also -inf and NaN
+    const float t = fmaf(l, c_hi, m0);
     float w;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(d, c_lo, fmaf(d, c_hi, kMagic - t))));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(l, c_lo, fmaf(l, c_hi, m0 - t)) - phi));
     return __int_as_float(__float_as_int(w) + (__float_as_int(t) << 23));
+  }
+  // What a - s z (a: a sum of some of the weights that z sums) may be off by: the
+  // errors of a count 1 - s times, those of the others s times.
+  __device__ static double off_by(double s, double a, double z) {
+    return kErr * ((1.0 - s) * a + s * fmax(z - a, 0.0)) + 1e-9 * z;
   }
 };
 
@@ -550,7 +571,6 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
   uint64_t* mine = list + warp * kPart;
   int n = 0;
   Sum2 tail;
-  float s1 = 0.0f;
 #pragma unroll 1
   for (int j0 = r.seg0; j0 < r.seg1; j0 += 128) {
     const int j = j0 + lane * 4;
@@ -560,14 +580,13 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
 #pragma unroll
     for (int e = 0; e < 4; ++e) bal[e] = __ballot_sync(0xffffffffu, l[e] >= least);
     if (use_p && k <= 0) {
+      float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float d;
-        float w = wf(l[e], d);
-        w = l[e] >= least ? 0.0f : w;
-        s1 = fmaf(w, d, s1);
-        tail.add(w);
+        w[e] = wf(l[e]);
+        w[e] = l[e] >= least ? 0.0f : w[e];
       }
+      tail.add(w[0], w[1], w[2], w[3]);
     }
     if (bal[0] | bal[1] | bal[2] | bal[3]) {  // of the 128, a lane's four are neighbours
       const uint32_t lt = (1u << lane) - 1u;
@@ -628,8 +647,7 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
     } else {
       within = (double)block_reduce<NT>(sum, sm.red, Add{}, (int64_t)0);
       const double t = block_reduce<NT>(tail.value(), sm.red, Add{}, 0.0) * unit;
-      const double e = block_reduce<NT>((double)s1, sm.red, Add{}, 0.0) * we.c * unit;
-      const double err = Expo32::kErr * t - Expo32::kErrY * e;
+      const double err = Expo32::kErr * t;
       z_lo = within + t - err;
       z_hi = within + t + err;
     }
@@ -702,7 +720,7 @@ struct Cut {
   int k, b1, b2, bk;  // top-k's bin; the bracket of top-p's (without it: bk twice)
   int n1, cnt_above, cnt_bk;  // tokens in the bracket, before it, before bk
   bool fits;  // the tokens of the bracket and of bk can be sorted
-  double z_lo, z_hi;  // bounds of all tokens' mass (top-p)
+  double z;  // the sum of all tokens' fp32 weights (top-p alone)
 
   // Rounded to the nearest bin: never falls where l falls, which is all that is
   // asked of it; a float, so comparing needs no conversion.  Not clamped to the
@@ -727,15 +745,12 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   if (mp > 0.0f)
     wmin = EXACT ? (A)__double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << p.sh)) : (A)fminf(mp, 1.0f);
   const bool use_m = mp > 0.0f;
-  // a token's weight; fp32: its share of the error bound, and whether min-p is open
-  float s1 = 0.0f;
-  bool open = false;
+  bool open = false;  // fp32: a weight too near min-p's border
   auto weight = [&](float l) -> A {
     if constexpr (EXACT) {
       return we(l);
     } else {
-      float y;
-      return (A)wf(l, y);
+      return (A)wf(l);
     }
   };
   // a bin as a bound of fbin: with top-k the last one took in all beyond it
@@ -748,7 +763,6 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   __syncthreads();
   bool good = q.fits;
   A za = 0, zt = 0, mass = 0;  // before the bracket; all that top-p's share is of; kept of the segment
-  double e1 = 0.0;             // sum of w |y|
   Sum2 as, ts, ms;
   if (good) {
     if constexpr (EXACT) {
@@ -781,9 +795,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
       }
     } else if (!q.bins) {
       walk4<1>(r, [&](int, const float4& v) {
-        float y0, y1, y2, y3;
-        float w0 = wf(v.x, y0), w1 = wf(v.y, y1), w2 = wf(v.z, y2), w3 = wf(v.w, y3);
-        s1 = fmaf(w0, y0, fmaf(w1, y1, fmaf(w2, y2, fmaf(w3, y3, s1))));
+        float w0 = wf(v.x), w1 = wf(v.y), w2 = wf(v.z), w3 = wf(v.w);
         if (use_m) {
           const float m = (float)wmin, near = m * 1e-5f;
           open = open || fabsf(w0 - m) <= near || fabsf(w1 - m) <= near || fabsf(w2 - m) <= near ||
@@ -793,10 +805,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
           w2 = w2 >= m ? w2 : 0.0f;
           w3 = w3 >= m ? w3 : 0.0f;
         }
-        ms.add(w0);
-        ms.add(w1);
-        ms.add(w2);
-        ms.add(w3);
+        ms.add(w0, w1, w2, w3);
       });
     } else {
       // tokens past the bracket (with top-k: past its bin) need no weight: without
@@ -809,25 +818,21 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
         float a[4], t[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float y;
-          const float w = wf(l[e], y);
-          s1 = fmaf(w, y, s1);
+          const float w = wf(l[e]);
           a[e] = b[e] < f1 ? w : 0.0f;
           t[e] = b[e] > f2 && b[e] < fk ? w : 0.0f;
           if (!(b[e] < f1) && listed(l[e], b[e])) sm.cand[atomicAdd(&sm.ncand, 1)] = code_of(l[e], j + e);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) as.add(a[e]);
-        if (q.use_k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ts.add(t[e]);
+        as.add(a[0], a[1], a[2], a[3]);
+        if (q.use_k) ts.add(t[0], t[1], t[2], t[3]);
         if (use_m) {
           const float m = (float)wmin;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             open = open || fabsf(a[e] - m) <= m * 1e-5f;
-            ms.add(a[e] >= m ? a[e] : 0.0f);
+            a[e] = a[e] >= m ? a[e] : 0.0f;
           }
+          ms.add(a[0], a[1], a[2], a[3]);
         }
       });
     }
@@ -840,7 +845,6 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
   }
   uint64_t cutcode = 0;  // kept: the tokens with at least this code
-  A z_all = 0;
   if (good && q.bins) {
     __syncthreads();
     const int nc = sm.ncand, P = pow2_from(nc);
@@ -856,17 +860,10 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     // how many candidates top-k leaves, then top-p
     int cut = nc;
     if (q.use_k) cut = q.bk > q.b2 ? q.n1 + (q.k - q.cnt_bk) : q.k - q.cnt_above;
-    z_all = zt + (nc > 0 ? cums[nc - 1] : A(0));
-    double err = 0.0;
-    if constexpr (!EXACT) {
-      e1 = block_reduce<NT>((double)s1 * (double)wf.c_hi, sm.red, Add{}, 0.0);
-      err = 2.0 * (Expo32::kErr * z_all - Expo32::kErrY * e1);
-    }
     if (q.use_p) {
-      const double pp = tp > 0.0f ? (double)tp : 0.0, z = (double)(zt + (cut > 0 ? cums[cut - 1] : A(0)));
-      const bool range = !EXACT && !q.use_k;
-      const double want = pp * (range ? 0.5 * (q.z_lo + q.z_hi) : z);
-      if (range) err += pp * 0.5 * (q.z_hi - q.z_lo);
+      const double pp = tp > 0.0f ? (double)tp : 0.0, zk = (double)(zt + (cut > 0 ? cums[cut - 1] : A(0)));
+      const double z = EXACT || q.use_k ? zk : q.z;  // (without top-k the fp32 pass stops at the bracket)
+      const double want = pp * z;
       int lo = 0, hi = min(q.n1, cut);  // candidates with less than `want` before them
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
@@ -881,12 +878,13 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
               (q.n1 > 0 && (double)(za + cums[q.n1 - 1]) >= want));
       if (!EXACT && good) {  // and no token's border is within the error of what is wanted
         auto before = [&](int i) { return (double)(za + (i ? cums[i - 1] : A(0))); };
+        auto err = [&](double a) { return Expo32::off_by(pp, a, z); };
         if (lo == 0)
           good = q.cnt_above == 0;
         else
-          good = want - before(lo - 1) > err || (lo == 1 && q.cnt_above == 0);
+          good = want - before(lo - 1) > err(before(lo - 1)) || (lo == 1 && q.cnt_above == 0);
         if (lo < min(q.n1, cut) || (lo == q.n1 && !(q.use_k && q.b2 == q.bk)))
-          good = good && before(lo) - want > err;
+          good = good && before(lo) - want > err(before(lo));
       }
       cut = q.cnt_above == 0 ? max(lo, 1) : lo;
     }
@@ -926,7 +924,6 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   }
   if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = mass;
   if constexpr (!EXACT) {
-    if (!q.bins) e1 = block_reduce<NT>((double)s1 * (double)wf.c_hi, sm.red, Add{}, 0.0);
     if (use_m && __syncthreads_or(open)) return false;
   }
   __syncthreads();
@@ -935,8 +932,6 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   const A total = __shfl_sync(0xffffffffu, sc, 31);
   const double target = (u > 0.0f ? (double)u : 0.0) * (double)total;
   const bool last = EXACT && target >= (double)total;  // u >= 1: the last kept token
-  // fp32: what a sum may be off by, with the target's own error (all tokens' mass bounds the kept ones')
-  const double slack = EXACT ? 0.0 : 2.0 * (Expo32::kErr * (double)(q.bins ? z_all : total) - Expo32::kErrY * e1);
   auto kept = [&](int j, int end) -> A {
     if (j < r.off || j >= end) return A(0);
     const float l = r.base[j];
@@ -974,7 +969,8 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
           // the token's borders; the first token's lower and the last one's upper are certain
           const double up = (double)__shfl_sync(0xffffffffu, run + cum, h),
                        down = (double)__shfl_sync(0xffffffffu, run + cum - w, h);
-          if (!(up - target > slack) || !(target - down > slack)) pick = -1;
+          const double s = fmin(fmax((double)u, 0.0), 1.0), z = (double)total;
+          if (!(up - target > Expo32::off_by(s, up, z)) || !(target - down > Expo32::off_by(s, down, z))) pick = -1;
         }
         if (!last) break;
       }
@@ -1143,6 +1139,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
   }
 
   if (k >= p.V) k = 0;
+  bool far_cut = false;
   if ((use_p || k > 0 || mp > 0.0f) && T <= 4.0f && Expo32::usable(mx, T)) {
     // How far from the maximum to list: min-p's reach where that is the only filter,
     // else what about five eighths of the list hold, judged by the first 128 tokens
@@ -1161,9 +1158,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       uint32_t far = 0u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float d;
-        const uint32_t m = (uint32_t)(wf(l[e], d) * 1048576.0f);
-        const float step = -d * (4.0f / T);
+        const uint32_t m = (uint32_t)(wf(l[e]) * 1048576.0f);
+        const float step = (mx - fmaxf(l[e], wf.least)) * (4.0f / T);
         if (step < 64.0f) {
           atomicAdd(&sm.h.cnt[(int)step], 1u);
           atomicAdd(&sm.h.lo[(int)step], m);
@@ -1181,8 +1177,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       const int64_t near = __reduce_max_sync(0xffffffffu, (uint32_t)(cb + c1 <= most ? mb + m1 : cb + c0 <= most ? mb + m0 : 0));
       least = mx - 0.25f * T * (float)steps;
       const double scale = (double)r.per / min(r.per, 128);
-      enough = steps > 0 && (k > 0 ? k <= most * scale
-                                   : near * scale + 1048576.0 > 0.9 * tp * ((all + rest) * scale + 1048576.0));
+      const double z = (all + rest) * scale + 1048576.0, want = tp * z - 1048576.0;
+      // (the sample knows the tail's share, of many tokens, better than the head's)
+      enough = steps > 0 && (k > 0 ? k <= most * scale : near * scale + 1048576.0 > (1.25 * tp - 0.25) * z);
+      far_cut = __popc(__ballot_sync(0xffffffffu, (mb + m1) * scale < want)) >= 15;  // past 7.5 T
     }
     __syncthreads();
     if (enough && pick_from_top<NT>(r, k, tp, mp, u, T, least, weight, list, sm, p, row)) return;
@@ -1192,7 +1190,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
   q.use_p = use_p;
   q.use_k = k > 0;
   // Top-p alone: the histogram covers what weighs e^-8 and more, where the cut
-  // mostly is (the tail's mass is summed aside), or else down to 2^-32.
+  // mostly is, or else down to 2^-32.
   float spread = INFINITY;
   if (q.use_k || T > 4.0f) {
     int nf = 0;
@@ -1209,11 +1207,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
   q.k = q.use_k ? k : 0;
   q.bins = q.use_k || use_p;
   q.b1 = q.b2 = q.bk = kBins;
-  q.z_lo = q.z_hi = 0.0;
+  q.z = 0.0;
   q.n1 = q.cnt_above = q.cnt_bk = 0;
   q.fits = true;
   if (q.bins && !(mx < INFINITY)) q.fits = false;
-  for (int turn = 0; q.bins && q.fits && turn < 2; ++turn) {
+  for (int turn = far_cut ? 1 : 0; q.bins && q.fits && turn < 2; ++turn) {
     // with top-k, what is farther shares the last bin
     const float range = q.use_k ? fminf(spread, 128.0f) : fminf(spread, (turn == 0 ? 8.0f : 22.5f) * T);
     q.scale = range > 0.0f ? fminf((float)(kBins - 1) / range, 1e30f) : 0.0f;
@@ -1227,21 +1225,22 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     __syncthreads();
     const Expo32 wf(mx, sm.c, T);
     const float unit = (float)(1u << (2 * p.half));
-    int64_t tail = 0;
+    Sum2 all;
     walk4<1>(r, [&](int, const float4& v) {
       const float l[4] = {v.x, v.y, v.z, v.w};
-      uint32_t m[4];
+      uint32_t m[4] = {0u, 0u, 0u, 0u};
       float b[4];
+      if (use_p) {
+        const float w[4] = {wf(v.x), wf(v.y), wf(v.z), wf(v.w)};
+        if (!q.use_k) all.add(w[0], w[1], w[2], w[3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float y;
-        m[e] = use_p ? (uint32_t)(wf(l[e], y) * unit) : 0u;  // 0 for -inf and NaN
-        b[e] = q.fbin(l[e]);
+        for (int e = 0; e < 4; ++e) m[e] = (uint32_t)(w[e] * unit);  // 0 for -inf and NaN
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = q.fbin(l[e]);
       // (-inf and NaN fall out of every bin; with top-k only NaN and -inf beyond a bin's reach do)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (!q.use_k) tail += b[e] <= Cut::kFar ? 0u : m[e];
         if (q.use_k ? l[e] > -INFINITY : b[e] <= Cut::kFar) {
           const int at = __float_as_int(fminf(b[e], Cut::kFar)) - 0x4b000000;
           atomicAdd(&sm.h.cnt[at], 1u);
@@ -1264,16 +1263,14 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       ms[e] = mass;
     }
     const int64_t c0 = block_scan<NT>(cs, sm.red) - cs;
-    int64_t m0 = 0, m_all = 0;
+    int64_t m0 = 0;
     if (use_p) {
-      tail = q.use_k ? 0 : block_reduce<NT>(tail, sm.red, Add{}, (int64_t)0);
+      q.z = q.use_k ? 0.0 : block_reduce<NT>(all.value(), sm.red, Add{}, 0.0);
       m0 = block_scan<NT>(mass, sm.red) - mass;
       if (tid == NT - 1) {
-        sm.seg[0] = sm.seg[1] = m0 + mass + tail;
+        sm.seg[0] = sm.seg[1] = q.use_k ? 0 : (int64_t)(q.z * (double)unit);
         sm.seg[2] = m0 + mass;  // the bins'
       }
-      __syncthreads();
-      m_all = sm.seg[0];
     }
     // sm.seg[0, 1]: mass before and with the last bin that counts
     __syncthreads();
@@ -1322,22 +1319,17 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     __syncthreads();
     q.cnt_above = sm.cnt_b1;
     q.n1 = sm.cnt_b2 - q.cnt_above;
-    const double per1 = 1.0 / (double)(1u << (2 * p.half));
-    q.z_lo = (double)m_all * per1 * (1.0 - Expo32::kHist);
-    q.z_hi = ((double)m_all + p.V) * per1 * (1.0 + Expo32::kHist);
     const int in_bk = q.use_k ? (int)sm.h.cnt[q.bk] : 0;
     q.fits = q.n1 + (q.use_k && q.bk > q.b2 ? in_bk : 0) <= NT;
     __syncthreads();
     if (!q.use_k && q.cnt_above + q.n1 <= NT && Expo32::usable(mx, T)) {
-      // A small nucleus: all its tokens fit the list, and the mass from the
-      // histogram (off by less than kHist and a unit a token) settles the cut
-      // unless it falls that close to a token's border.
+      // A small nucleus: all its tokens fit the list, and the fp32 mass of all tokens
+      // settles the cut unless it falls within its error of a token's border.
       const float edge = Cut::kOne + (float)q.b2;  // (b2 is the last bin: what is past it weighs nothing)
       collect<NT, 2>(r, list, sm.cand, NT, &sm.ncand,
                      [&](float l) { return l > -INFINITY && q.fbin(l) <= edge; });
-      const double per = sh >= 2 * p.half ? (double)((int64_t)1 << (sh - 2 * p.half)) : 1.0 / (double)(1 << (2 * p.half - sh));
-      const int64_t z_lo = (int64_t)((double)m_all * per * (1.0 - Expo32::kHist)),
-                    z_hi = (int64_t)(((double)m_all + p.V) * per * (1.0 + Expo32::kHist)) + 1;
+      const double z = q.z * (double)((int64_t)1 << sh);
+      const int64_t z_lo = (int64_t)(z * (1.0 - Expo32::kErr)), z_hi = (int64_t)(z * (1.0 + Expo32::kErr)) + 1;
       if (pick_from_list<NT>(q.cnt_above + q.n1, INT_MAX, tp, z_lo, z_hi, wmin, u, weight, T, sm, p, row, r.off))
         return;
       __syncthreads();

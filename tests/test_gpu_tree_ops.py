@@ -364,6 +364,34 @@ def test_sample_logits_of_any_spread(gpu, scale):
             _check_sample(l, u, tok, lp, np.full(M, T), **kw)
 
 
+@pytest.mark.parametrize("M", [24, 200])  # one row an SM, and several
+@pytest.mark.parametrize("how", ["plain", "p", "kp", "m"])
+def test_sample_at_the_borders(gpu, M, how):
+    """u (and top_p) as near to a border between two tokens as fp32 numbers come, some 1e-8 of the mass."""
+    V = 32768
+    rng = np.random.default_rng(M + len(how))
+    l = (1.5 * rng.standard_normal((M, V)) + rng.exponential(1.2, (M, V))).astype(np.float32)
+    kw = {"p": dict(top_p=np.zeros(M)), "kp": dict(top_p=np.zeros(M), top_k=np.full(M, 9000)), "m": dict(min_p=np.full(M, 1e-3)),
+          "plain": {}}[how]
+    u = np.empty(M, np.float32)
+    for m in range(M):
+        w = np.exp(l[m].astype(np.float64) - l[m].max())
+        order = np.argsort(-l[m], kind="stable")
+        if how == "kp":
+            order = order[:9000]
+        if "top_p" in kw:  # between n and n + 1 tokens
+            cum = np.cumsum(w[order])
+            n = int(rng.integers(20, 0.9 * len(order)))
+            kw["top_p"][m] = np.float32(cum[n - 1] / cum[-1])
+            order = order[:n + int(kw["top_p"][m] > cum[n - 1] / cum[-1])]
+        if how == "m":
+            order = order[w[order] >= np.float32(1e-3)]
+        cum = np.cumsum(w[np.sort(order)])
+        u[m] = cum[rng.integers(0, max(1, len(cum) - 1))] / cum[-1]
+    tok, lp = _sample(gpu, l, u, **kw)
+    _check_sample(l, u, tok, lp, **kw)
+
+
 def test_sample_strided_rows_and_no_logprob(gpu):
     x = torch.randn((5, 4, 777), device=DEV)
     l = x[:, 2]

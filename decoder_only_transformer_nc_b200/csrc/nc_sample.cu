@@ -78,30 +78,25 @@ __device__ __forceinline__ double wide(float x) {
   return __hiloint2double(((u >> 3) & (int)0x8fffffffu) + (896 << 20), u << 29);
 }
 
-// A sum of weights (at most 1, a little more for rounding) in two fp32 parts: what
-// an addition rounds off is kept.  It starts at 8, so the sum is never the smaller
-// one, which makes the rounded-off part exact in two operations.  Four weights are
-// added up first, unless one may be the maximum's: what is beside a 1 counts in
-// full (the logprob of a token that is nearly certain).
-struct Sum2 {
-  float hi = 8.0f, lo = 0.0f;
-  __device__ __forceinline__ void add(float a, float b, float c, float d) {
+// The same of a weight, which is not negative.
+__device__ __forceinline__ double wide_weight(float x) {
+  const int u = __float_as_int(x);
+  return __hiloint2double((u >> 3) + (896 << 20), u << 29);
+}
+
+// A sum of fp32 weights in fp64.  Four are added up first, unless one may be the
+// maximum's (of weight `big` or more): what is beside it counts in full (the
+// logprob of a token that is nearly certain).
+struct Sum {
+  double v = 0.0;
+  __device__ __forceinline__ float add(float a, float b, float c, float d, float big = 1.0f) {
     const float x = (a + b) + (c + d);
-    if (x < 1.0f) {
-      add(x);
-    } else {
-      add(a);
-      add(b);
-      add(c);
-      add(d);
-    }
+    if (x < big)
+      v += wide_weight(x);
+    else
+      v += (wide_weight(a) + wide_weight(b)) + (wide_weight(c) + wide_weight(d));
+    return x;
   }
-  __device__ __forceinline__ void add(float x) {
-    const float t = hi + x;
-    lo += x - (t - hi);
-    hi = t;
-  }
-  __device__ __forceinline__ double value() const { return ((double)hi - 8.0) + (double)lo; }
 };
 
 // A row's exponential: exp((l - mx) / T) in units of 2^-sh, rounded to nearest.
@@ -163,6 +158,23 @@ struct Expo32 {
     const float t = fmaf(mx, c_hi, m0);
     phi = (t - kMagic) + fmaf(mx, c_lo, fmaf(mx, c_hi, m0 - t));
   }
+  Expo32() = default;
+  // Against 2^n0 (n0 an integer) instead of the maximum, for scaled().
+  __device__ static Expo32 against(float n0, float mx, double c, float T) {
+    Expo32 w;
+    w.c_hi = (float)c;
+    w.c_lo = (float)(c - (double)w.c_hi);
+    w.least = mx - 69.3f * T;
+    w.m0 = kMagic - n0;
+    return w;
+  }
+  __device__ __forceinline__ float scaled(float l) const {
+    l = fmaxf(l, least);
+    const float t = fmaf(l, c_hi, m0);
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(l, c_lo, fmaf(l, c_hi, m0 - t))));
+    return __int_as_float(__float_as_int(w) + (__float_as_int(t) << 23));
+  }
   __device__ static bool usable(float mx, float T) {
     return T > 1e-20f && T < 1e20f && fabsf(mx) < 1e5f * T;
   }
@@ -173,10 +185,28 @@ struct Expo32 {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(l, c_lo, fmaf(l, c_hi, m0 - t)) - phi));
     return __int_as_float(__float_as_int(w) + (__float_as_int(t) << 23));
   }
+  // The weight to 2.5e-9 in fp64: l log2(e) / T = n + j / 32 + g, |g| <= 1/64, with
+  // 2^(j / 32) in fp64 and 2^g - 1, at most 0.011, in fp32 (Taylor to the 4th power, the
+  // rest 1e-12; three roundings of 2^-24 of it, two of 2^-31 of g).
+  static constexpr double kErrFine = 3e-9;
+  __device__ __forceinline__ double fine(float l, float n0, const double* tab) const {
+    l = fmaxf(l, least);
+    const float m = fmaf(-32.0f, n0, kMagic);
+    const float t = fmaf(l, 32.0f * c_hi, m);
+    const float g = fmaf(l, c_lo, fmaf(l, c_hi, (m - t) * 0.03125f));
+    const int k = __float_as_int(t) - __float_as_int(kMagic);
+    // ln(2)^i / i!
+    float e = fmaf(9.618129e-3f, g, 5.5504109e-2f);
+    e = fmaf(e, g, 2.4022651e-1f);
+    e = fmaf(e, g, 6.9314718e-1f) * g;
+    double w = tab[k & 31];
+    w = __hiloint2double(__double2hiint(w) + ((k & ~31) << 15), __double2loint(w));
+    return fma(w, wide(e), w);
+  }
   // What a - s z (a: a sum of some of the weights that z sums) may be off by: the
   // errors of a count 1 - s times, those of the others s times.
-  __device__ static double off_by(double s, double a, double z) {
-    return kErr * ((1.0 - s) * a + s * fmax(z - a, 0.0)) + 1e-9 * z;
+  __device__ static double off_by(double s, double a, double z, double err = kErr) {
+    return err * ((1.0 - s) * a + s * fmax(z - a, 0.0)) + 1e-9 * z;
   }
 };
 
@@ -570,7 +600,7 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
   const Expo32 wf(we.mx, we.c, T);
   uint64_t* mine = list + warp * kPart;
   int n = 0;
-  Sum2 tail;
+  Sum tail;
 #pragma unroll 1
   for (int j0 = r.seg0; j0 < r.seg1; j0 += 128) {
     const int j = j0 + lane * 4;
@@ -646,7 +676,7 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
       z_lo = z_hi = within = (double)(mass_above(cut) + (int64_t)ties * we(value_of(cut)));
     } else {
       within = (double)block_reduce<NT>(sum, sm.red, Add{}, (int64_t)0);
-      const double t = block_reduce<NT>(tail.value(), sm.red, Add{}, 0.0) * unit;
+      const double t = block_reduce<NT>(tail.v, sm.red, Add{}, 0.0) * unit;
       const double err = Expo32::kErr * t;
       z_lo = within + t - err;
       z_hi = within + t + err;
@@ -713,6 +743,170 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
   return true;
 }
 
+// The token among the kept ones: the segment (sm.seg: every warp's kept mass) whose
+// part of the running mass holds u times the total, each warp's share of that
+// segment, and the position.  kept(position, logit): a token's mass.  EXACT: the
+// masses are integers; else fp32 weights, and the token is only named where the
+// errors leave its borders clear of the target.  The position in every lane of
+// the warp that finds it, -1 in the others.  For the whole block.
+template <int NT, bool EXACT, typename A, typename F>
+__device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& total, F kept,
+                                      double err = Expo32::kErr) {
+  constexpr int NW = NT / 32, U = EXACT ? 2 : 8;  // loads in flight
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const A sv = lane < NW ? *reinterpret_cast<const A*>(&sm.seg[lane]) : A(0), sc = warp_scan(sv);
+  total = __shfl_sync(0xffffffffu, sc, 31);
+  const double z = (double)total, target = (u > 0.0f ? (double)u : 0.0) * z;
+  const bool last = EXACT && target >= z;  // u >= 1: the last kept token
+  const uint32_t has = __ballot_sync(0xffffffffu, sv > A(0) && (last || (double)sc > target));
+  if (!EXACT && !has) return -1;
+  const int s = last ? 31 - __clz(has) : __ffs(has) - 1;
+  const A before = __shfl_sync(0xffffffffu, sc - sv, s);
+  const int sub = (r.per + NT - 1) / NT * 32;  // positions a warp
+  const int s0 = s * r.per + warp * sub, s1 = min(min(s0 + sub, (s + 1) * r.per), r.end);
+  float l[U];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const int i = j + e * 32 + lane;
+      l[e] = i >= r.off && i < s1 ? r.base[i] : NAN;
+    }
+  };
+  A part = 0;
+#pragma unroll 1
+  for (int j = s0; j < s1; j += 32 * U) {
+    load(j);
+#pragma unroll
+    for (int e = 0; e < U; ++e) part += kept(j + e * 32 + lane, l[e]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+  __syncthreads();
+  if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = part;
+  __syncthreads();
+  const A pv = lane < NW ? *reinterpret_cast<const A*>(&sm.seg[lane]) : A(0), pc = warp_scan(pv);
+  const uint32_t at = __ballot_sync(0xffffffffu, pv > A(0) && (last || (double)(before + pc) > target));
+  const int owner = at ? (last ? 31 - __clz(at) : __ffs(at) - 1) : -1;
+  if (warp != owner) return -1;
+  A run = before + __shfl_sync(0xffffffffu, pc - pv, warp);
+  int pick = -1;
+  bool found = false;
+#pragma unroll 1
+  for (int j = s0; j < s1 && (last || !found); j += 32 * U) {
+    load(j);
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const A w = kept(j + e * 32 + lane, l[e]), cum = warp_scan(w);
+      const uint32_t hit = __ballot_sync(0xffffffffu, w > A(0) && (last || (double)(run + cum) > target));
+      if (hit && (last || !found)) {
+        const int h = last ? 31 - __clz(hit) : __ffs(hit) - 1;
+        found = true;
+        pick = j + e * 32 + h;
+        if (!EXACT) {
+          // the token's borders; the first token's lower and the last one's upper are certain
+          const double up = (double)__shfl_sync(0xffffffffu, run + cum, h),
+                       down = (double)__shfl_sync(0xffffffffu, run + cum - w, h);
+          const double v = fmin(fmax((double)u, 0.0), 1.0);
+          if (!(up - target > Expo32::off_by(v, up, z, err)) || !(target - down > Expo32::off_by(v, down, z, err)))
+            pick = -1;
+        }
+      }
+      run += __shfl_sync(0xffffffffu, cum, 31);
+    }
+  }
+  return pick;
+}
+
+// The token where there is no filter: the logits are read once.  The weights are
+// counted against a power of two 2^12 (kRoom) or more above the largest of the first
+// tokens of every segment; should one of the rest be above that, the sums are not
+// valid and the answer is -1.  0 where the fp32 errors leave the token open (a row in
+// a hundred at 32768 tokens); FINE: for those, with fp64 weights.  Else 1.  For the
+// whole block.
+template <int NT, bool FINE>
+__device__ __noinline__ int pick_plain(const Row r, float u, float T, double c, Smem<NT>& sm, const SampleParams& p,
+                                        int row) {
+  constexpr int NW = NT / 32, U = 4, kRoom = 12;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float4 v[U];
+  const int j0 = r.seg0 + lane * 4;
+  auto load = [&](int j) {
+#pragma unroll
+    for (int e = 0; e < U; ++e)
+      v[e] = j + e * 128 < r.seg1 ? load4(r, j + e * 128) : make_float4(NAN, NAN, NAN, NAN);
+  };
+  load(j0);
+  float mx = -INFINITY;
+  auto upto = [&](const float4& x) { mx = fmaxf(mx, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w))); };  // ignores NaN
+#pragma unroll
+  for (int e = 0; e < U; ++e) upto(v[e]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) sm.redf[0][warp] = mx;
+  __syncthreads();
+  mx = lane < NW ? sm.redf[0][lane] : -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (!(mx > -INFINITY) || !Expo32::usable(mx, T)) return -1;
+  const float n0 = ceilf(mx * (float)c) + (float)kRoom;
+  const Expo32 wf = Expo32::against(n0, mx, c, T);
+  constexpr float kBig = 1.0f / (1 << (kRoom + 2));  // the maximum's weight is more
+  auto weight = [&](float l) -> double {
+    if constexpr (FINE)
+      return wf.fine(l, n0, sm.tab);
+    else
+      return wide_weight(wf.scaled(l));
+  };
+  Sum sum;
+  float most = 0.0f;
+#pragma unroll 1
+  for (int j = j0; j - lane * 4 < r.seg1;) {
+    float4 x[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) x[e] = v[e];
+    j += 128 * U;
+    if (j - lane * 4 < r.seg1) load(j);
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      upto(x[e]);
+      if constexpr (FINE)
+        sum.v += (weight(x[e].x) + weight(x[e].y)) + (weight(x[e].z) + weight(x[e].w));
+      else
+        most = fmaxf(most, sum.add(wf.scaled(x[e].x), wf.scaled(x[e].y), wf.scaled(x[e].z), wf.scaled(x[e].w), kBig));
+    }
+  }
+  double mass = sum.v;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  __syncthreads();
+  if (lane == 0) {
+    *reinterpret_cast<double*>(&sm.seg[warp]) = mass;
+    sm.redf[0][warp] = mx;
+  }
+  if (__syncthreads_or(most > 1.0f)) return -1;
+  double total;
+  const int pick = locate<NT, false>(
+      r, sm, u, total, [&](int, float l) { return l > -INFINITY ? weight(l) : 0.0; },
+      FINE ? Expo32::kErrFine : Expo32::kErr);
+  if (lane == 0 && pick >= 0) {
+    p.tokens[row] = pick - r.off;
+    if (p.logprob) {
+      // the token's weight and the largest enter in full: a token that is nearly certain
+      // has a logprob as exact as what is beside it
+      for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm.redf[0][w]);
+      const float l = r.base[pick];
+      const double y = fma((double)l, c, -(double)n0), w = exp2(y);
+      total += w - weight(l);
+      if (l != mx) total += exp2(fma((double)mx, c, -(double)n0)) - weight(mx);
+      p.logprob[row] = (float)-log(total / w);
+    }
+  }
+  return __syncthreads_or(pick >= 0) ? 1 : 0;
+}
+
 // What the histogram found out.
 struct Cut {
   bool bins, use_k, use_p;
@@ -750,7 +944,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     if constexpr (EXACT) {
       return we(l);
     } else {
-      return (A)wf(l);
+      return wide_weight(wf(l));
     }
   };
   // a bin as a bound of fbin: with top-k the last one took in all beyond it
@@ -763,7 +957,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   __syncthreads();
   bool good = q.fits;
   A za = 0, zt = 0, mass = 0;  // before the bracket; all that top-p's share is of; kept of the segment
-  Sum2 as, ts, ms;
+  Sum as, ts, ms;
   if (good) {
     if constexpr (EXACT) {
       uint64_t sum = 0;  // modulo 2^64 until the 2^52 of every position is taken off
@@ -837,9 +1031,9 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
       });
     }
     if constexpr (!EXACT) {
-      za = as.value();
-      zt = za + ts.value();
-      mass = q.bins && !use_m ? za : ms.value();
+      za = as.v;
+      zt = za + ts.v;
+      mass = q.bins && !use_m ? za : ms.v;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
@@ -927,68 +1121,22 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     if (use_m && __syncthreads_or(open)) return false;
   }
   __syncthreads();
-  // the segment that holds the token (every warp finds it), then the warp's share of it
-  const A sv = lane < NW ? *reinterpret_cast<const A*>(&sm.seg[lane]) : A(0), sc = warp_scan(sv);
-  const A total = __shfl_sync(0xffffffffu, sc, 31);
-  const double target = (u > 0.0f ? (double)u : 0.0) * (double)total;
-  const bool last = EXACT && target >= (double)total;  // u >= 1: the last kept token
-  auto kept = [&](int j, int end) -> A {
-    if (j < r.off || j >= end) return A(0);
-    const float l = r.base[j];
+  auto kept = [&](int j, float l) -> A {
     if (!(l > -INFINITY) || code_of(l, j) < cutcode) return A(0);
     const A w = weight(l);
     return w >= wmin ? w : A(0);
   };
-  const uint32_t has = __ballot_sync(0xffffffffu, sv > A(0) && (last || (double)sc > target));
-  if (!EXACT && !has) return false;
-  const int s = last ? 31 - __clz(has) : __ffs(has) - 1;
-  const A before = __shfl_sync(0xffffffffu, sc - sv, s);
-  const int sub = (r.per + NT - 1) / NT * 32;  // positions a warp
-  const int s0 = s * r.per + warp * sub, s1_ = min(min(s0 + sub, (s + 1) * r.per), r.end);
-  A part = 0;
-  for (int j = s0; j < s1_; j += 32) part += kept(j + lane, s1_);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  __syncthreads();
-  if (lane == 0) *reinterpret_cast<A*>(&sm.seg[warp]) = part;
-  if (tid == 0) sm.pick = 0;
-  __syncthreads();
-  const A pv = lane < NW ? *reinterpret_cast<const A*>(&sm.seg[lane]) : A(0), pc = warp_scan(pv);
-  const uint32_t at = __ballot_sync(0xffffffffu, pv > A(0) && (last || (double)(before + pc) > target));
-  const int owner = at ? (last ? 31 - __clz(at) : __ffs(at) - 1) : -1;
-  A run = before + __shfl_sync(0xffffffffu, pc - pv, warp);
-  if (warp == owner) {
-    int pick = -1;
-    for (int j = s0; j < s1_; j += 32) {
-      const A w = kept(j + lane, s1_), cum = warp_scan(w);
-      const uint32_t hit = __ballot_sync(0xffffffffu, w > A(0) && (last || (double)(run + cum) > target));
-      if (hit) {
-        const int h = last ? 31 - __clz(hit) : __ffs(hit) - 1;
-        pick = j + h;
-        if (!EXACT) {
-          // the token's borders; the first token's lower and the last one's upper are certain
-          const double up = (double)__shfl_sync(0xffffffffu, run + cum, h),
-                       down = (double)__shfl_sync(0xffffffffu, run + cum - w, h);
-          const double s = fmin(fmax((double)u, 0.0), 1.0), z = (double)total;
-          if (!(up - target > Expo32::off_by(s, up, z)) || !(target - down > Expo32::off_by(s, down, z))) pick = -1;
-        }
-        if (!last) break;
-      }
-      run += __shfl_sync(0xffffffffu, cum, 31);
-    }
-    if (lane == 0 && pick >= 0) {
-      const float l = r.base[pick];
-      p.tokens[row] = pick - r.off;
-      if (p.logprob) {
-        const double z = EXACT ? log((double)total) - (double)p.sh * 0.6931471805599453 : log((double)total);
-        p.logprob[row] = (float)((l == q.mx ? 0.0 : ((double)l - (double)q.mx) / (double)T) - z);
-      }
-      sm.pick = 1;
+  A total;
+  const int pick = locate<NT, EXACT>(r, sm, u, total, kept);
+  if (lane == 0 && pick >= 0) {
+    const float l = r.base[pick];
+    p.tokens[row] = pick - r.off;
+    if (p.logprob) {
+      const double z = EXACT ? log((double)total) - (double)p.sh * 0.6931471805599453 : log((double)total);
+      p.logprob[row] = (float)((l == q.mx ? 0.0 : ((double)l - (double)q.mx) / (double)T) - z);
     }
   }
-  if constexpr (EXACT) return true;
-  __syncthreads();
-  return sm.pick != 0;
+  return EXACT || __syncthreads_or(pick >= 0);
 }
 
 // One CTA a row.  STAGED: the row is kept in shared memory after its first pass.
@@ -1016,8 +1164,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
   const float tp = p.top_p ? p.top_p[row] : 1.0f;
   const float mp = p.min_p ? p.min_p[row] : 0.0f;
 
-  // the maximum; the smallest of the threads' maxima
-  float my_max = -INFINITY;
   bool late = false;  // the copy did not arrive
   if (STAGED) {
     // each warp's segment by one asynchronous copy of its own, the row's first and
@@ -1043,6 +1189,24 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       while (!late && !mbar_try_wait(smem_u32(&sm.bar[warp]), 0)) late = global_timer_ns() - t0 > kWaitLimitNs;
     }
   }
+  if (T > 0.0f && u < 1.0f && tp >= 1.0f && !(mp > 0.0f) && (k <= 0 || k >= p.V)) {
+    if (__syncthreads_or(late)) {
+      if (tid == 0) {
+        p.tokens[row] = -1;
+        if (p.logprob) p.logprob[row] = NAN;
+      }
+      return;
+    }
+    int done = pick_plain<NT, false>(r, u, T, sm.c, sm, p, row);
+    __syncthreads();
+    if (done == 0) {
+      done = pick_plain<NT, true>(r, u, T, sm.c, sm, p, row);
+      __syncthreads();
+    }
+    if (done > 0) return;
+  }
+  // the maximum; the smallest of the threads' maxima
+  float my_max = -INFINITY;
   walk4<4>(r, [&](int j, const float4& v) {
     my_max = fmaxf(my_max, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));  // ignores NaN
   });
@@ -1225,7 +1389,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     __syncthreads();
     const Expo32 wf(mx, sm.c, T);
     const float unit = (float)(1u << (2 * p.half));
-    Sum2 all;
+    Sum all;
     walk4<1>(r, [&](int, const float4& v) {
       const float l[4] = {v.x, v.y, v.z, v.w};
       uint32_t m[4] = {0u, 0u, 0u, 0u};
@@ -1265,7 +1429,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     const int64_t c0 = block_scan<NT>(cs, sm.red) - cs;
     int64_t m0 = 0;
     if (use_p) {
-      q.z = q.use_k ? 0.0 : block_reduce<NT>(all.value(), sm.red, Add{}, 0.0);
+      q.z = q.use_k ? 0.0 : block_reduce<NT>(all.v, sm.red, Add{}, 0.0);
       m0 = block_scan<NT>(mass, sm.red) - mass;
       if (tid == NT - 1) {
         sm.seg[0] = sm.seg[1] = q.use_k ? 0 : (int64_t)(q.z * (double)unit);

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "nc_half.cuh"
 #include "nc_internal.h"
@@ -33,6 +34,41 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// The maximum over the warp (NaN gives way).
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// Pairs of fp32: the kernel is bound by the instructions it issues.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); }
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -59,6 +95,7 @@ __device__ __forceinline__ float tanh_far(float u) {
 // tanh(z / cap) with the quotient's coefficients in terms of z.
 struct Tanh {
   float inv_cap, near, a1, a2, b1, b2, b3;
+  float2 pi, pa1, pa2, pb1, pb2, pb3;  // each twice, for pairs
   explicit Tanh(float cap) {
     inv_cap = 1.0f / cap;
     near = kNear * cap;
@@ -68,6 +105,12 @@ struct Tanh {
     b1 = 4725.0f / 10395.0f * c2;
     b2 = 210.0f / 10395.0f * (c2 * c2);
     b3 = 1.0f / 10395.0f * (c2 * c2 * c2);
+    pi = make_float2(inv_cap, inv_cap);
+    pa1 = make_float2(a1, a1);
+    pa2 = make_float2(a2, a2);
+    pb1 = make_float2(b1, b1);
+    pb2 = make_float2(b2, b2);
+    pb3 = make_float2(b3, b3);
   }
   __device__ __forceinline__ float close(float z) const {
     const float s = z * z;
@@ -78,9 +121,16 @@ struct Tanh {
   __device__ __forceinline__ float operator()(float z) const {
     return fabsf(z) <= near ? close(z) : tanh_far(z * inv_cap);
   }
+  __device__ __forceinline__ uint64_t close2(uint64_t z) const {
+    const uint64_t s = mul2(z, z);
+    const uint64_t a = fma2(fma2(pair(pa2), s, pair(pa1)), s, pair(pi));
+    const float2 b = unpair(fma2(fma2(fma2(pair(pb3), s, pair(pb2)), s, pair(pb1)), s, pair(1.0f, 1.0f)));
+    return mul2(mul2(z, a), pair(rcp(b.x), rcp(b.y)));
+  }
   // four at a time; the far form only where some lane of the warp needs it
   __device__ __forceinline__ float4 operator()(const float4& z) const {
-    float4 t = make_float4(close(z.x), close(z.y), close(z.z), close(z.w));
+    const float2 t01 = unpair(close2(pair(z.x, z.y))), t23 = unpair(close2(pair(z.z, z.w)));
+    float4 t = make_float4(t01.x, t01.y, t23.x, t23.y);
     const float m = fmaxf(fmaxf(fabsf(z.x), fabsf(z.y)), fmaxf(fabsf(z.z), fabsf(z.w)));
     if (!(m <= near)) {
       if (!(fabsf(z.x) <= near)) t.x = tanh_far(z.x * inv_cap);
@@ -105,11 +155,14 @@ struct DistillParams {
   uint32_t* status;
 };
 
-// (maximum, sum) of two parts of a softmax, log2 domain.
-__device__ __forceinline__ float2 join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x);
-  if (m == -INFINITY) return make_float2(m, 0.0f);
-  return make_float2(m, fmaf(a.y, ex2(a.x - m), b.y * ex2(b.x - m)));
+// (maximum, sum) of the parts of a softmax that the first n <= 8 lanes hold (log2
+// domain), in a fixed tree, in every one of the first 8 lanes.
+__device__ __forceinline__ float2 join8(float2 v) {
+  const float m = warp_max_redux(v.x);
+  float s = m == -INFINITY ? 0.0f : v.y * ex2(v.x - m);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return make_float2(m, s);
 }
 
 // A row is dealt over the CTAs of a cluster (one CTA up to 8192 logits), every
@@ -135,13 +188,51 @@ __device__ __forceinline__ void named_arrive(int id, int n) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
+// Built-in indices that are read anew: what depends on them is computed where it is
+// used, not kept in registers (or spilled) from the row's loads to the gradient's
+// stores.
+__device__ __forceinline__ uint32_t fresh_tid() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t fresh_row() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%ctaid.y;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t fresh_rank() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(v));
+  return v;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Of a thread's groups, how many are in registers, and the CTAs that share an SM.
+// With a gradient, half of the eight are in shared memory: with all of them in registers four
+// CTAs fit an SM, and spill (225 us for 4096 rows of 32768 logits, K = 64, bf16 gradient;
+// so 201).  Without, the row's values are needed once less (59 us for 2048 rows, 65).
+constexpr int held(int dz, int regs) { return dz != 0 && regs == 8 ? 4 : regs; }
+constexpr int resident(int dz, int regs) { return regs != 8 ? 1 : dz != 0 ? 5 : 4; }
+
+constexpr int kTwice = 1 << 30;  // marks an index of the table (below 2^24)
+
 // FULL: every thread has REGS whole groups (no test of a group's place).
 template <int DZ, bool CAP, int REGS, bool FULL>
-__device__ __forceinline__ void distill_part(const DistillParams& p, int slice, int slots, float* q_s, Shared& sh) {
-  //  // [K] logits, then probabilities; [K] z of the entry; [K] indices; [slots]
+__device__ __forceinline__ void distill_part(const DistillParams& p, int slice, int slots, float* mem, Shared& sh) {
+  // mem: the groups not in registers; the teacher's [K] logits, [K] z at the entry,
+  // [K] indices; [K] the entries of this CTA's positions, [K] their gradients; [slots]
+  constexpr int HELD = held(DZ, REGS);
+  float4* own = reinterpret_cast<float4*>(mem) + threadIdx.x;  // this thread's, kThreads apart
+  float* q_s = mem + (REGS - HELD) * kThreads * 4;
   float* z_s = q_s + p.K;
   int32_t* i_s = reinterpret_cast<int32_t*>(z_s + p.K);
-  int32_t* table = i_s + p.K;
+  int32_t* list = i_s + p.K;
+  float* g_s = reinterpret_cast<float*>(i_s + 2 * p.K);
+  int32_t* table = i_s + 3 * p.K;
   const int64_t row = blockIdx.y;
   const int rank = blockIdx.x, CS = gridDim.x;  // the cluster spans the grid's x
   const int V = p.V, K = p.K, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -165,17 +256,35 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
   const int j_first = s0 + tid * 4;
   // groups of this thread (0 or less: none)
   const int nr = warp == kThreads / 32 ? 0 : (s1 - j_first + STEP - 1) / STEP;
-  float4 keep[REGS > 0 ? REGS : 1];
+  float4 keep[HELD > 0 ? HELD : 1];
   if constexpr (REGS > 0) {
 #pragma unroll
-    for (int r = 0; r < REGS; ++r)
+    for (int r = HELD; r < REGS; ++r) {
+      if (FULL) {
+        if (warp < kThreads / 32) cp_async16(own + (r - HELD) * kThreads, z + j_first + r * STEP);
+      } else if (r < nr) {
+        own[(r - HELD) * kThreads] = load(j_first + r * STEP);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < HELD; ++r)
       if (FULL ? warp < kThreads / 32 : r < nr) keep[r] = load(j_first + r * STEP);
   }
-  auto each = [&](auto f) {
+  // f(position, four values); WRITE: f changes them
+  auto each = [&](int j_first, auto write, auto f) {
     if constexpr (REGS > 0) {
+      constexpr bool WRITE = decltype(write)::value;
 #pragma unroll
-      for (int r = 0; r < REGS; ++r)
+      for (int r = 0; r < HELD; ++r)
         if (FULL || r < nr) f(j_first + r * STEP, keep[r]);
+      if (FULL && WRITE && REGS > HELD) asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+      for (int r = HELD; r < REGS; ++r)
+        if (FULL || r < nr) {
+          float4 v = own[(r - HELD) * kThreads];
+          f(j_first + r * STEP, v);
+          if (WRITE) own[(r - HELD) * kThreads] = v;
+        }
     } else {
 #pragma unroll 1
       for (int j = j_first, r = 0; r < nr; ++r, j += STEP) {
@@ -187,53 +296,52 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
 
   // the teacher's softmax, while the row is on its way
   const bool helper = warp == kThreads / 32;
-  bool t_any = true, t_twice = false;  // the helper's
+  bool t_any = true;  // the helper's
   float t_lse = 0.0f;
+  int n_here = 0;  // entries of this CTA's positions
   if (helper) {
     float tm = -INFINITY;
-    for (int k = lane; k < slots; k += 32) table[k] = -1;
-    for (int k = lane; k < K; k += 32) {
-      int i = p.idx[row * K + k];
-      if (i < -1 || i >= V) {
-        if (p.status) atomicOr(p.status, NC_DEV_TARGET_RANGE);
-        i = -1;
+    for (int k0 = 0; k0 < K; k0 += 32) {
+      const int k = k0 + lane;
+      int i = -1;
+      if (k < K) {
+        i = p.idx[row * K + k];
+        if (i < -1 || i >= V) {
+          if (p.status) atomicOr(p.status, NC_DEV_TARGET_RANGE);
+          i = -1;
+        }
+        const float t = i < 0 ? -INFINITY : p.teacher[row * K + k] * p.inv_tau;
+        z_s[k] = i < 0 ? 0.0f : zr[i];
+        i_s[k] = i;
+        q_s[k] = t;
+        tm = fmaxf(tm, t);
       }
-      const float t = i < 0 ? -INFINITY : p.teacher[row * K + k] * p.inv_tau;
-      z_s[k] = i < 0 ? 0.0f : zr[i];
-      i_s[k] = i;
-      q_s[k] = t;
-      tm = fmaxf(tm, t);
+      if (DZ != 0) {
+        const bool here = i >= 0 && off + i >= s0 && off + i < s1;
+        const uint32_t bal = __ballot_sync(0xffffffffu, here);
+        if (here) list[n_here + __popc(bal & ((1u << lane) - 1u))] = k;
+        n_here += __popc(bal);
+      }
     }
-    tm = warp_max(tm);
+    tm = warp_max_redux(tm);
     const bool any = tm != -INFINITY;
     float ts = 0.0f;
     for (int k = lane; k < K; k += 32) ts += any ? expf(q_s[k] - tm) : 0.0f;
     ts = warp_sum(ts);
-    bool twice = false;
-    if (DZ != 0) {  // is an index given more than once?  (a table of 2 K slots or more)
-      __syncwarp();
-      for (int k = lane; k < K; k += 32) {
-        const int i = i_s[k];
-        for (int h = i; i >= 0; ++h) {
-          const int was = atomicCAS(&table[h & (slots - 1)], -1, i);
-          twice = twice || was == i;
-          if (was == -1 || was == i) break;
-        }
-      }
-      twice = __any_sync(0xffffffffu, twice);
-    }
     t_any = any;
-    t_twice = twice;
     t_lse = any ? tm + logf(ts) : 0.0f;
   }
 
   // the student's softmax: with registers, t takes the place of z
   float2 ms = make_float2(-INFINITY, 0.0f);
-  auto sum4 = [&](const float4& v, float m) {
-    return (ex2(fmaf(v.x, kx, -m)) + ex2(fmaf(v.y, kx, -m))) + (ex2(fmaf(v.z, kx, -m)) + ex2(fmaf(v.w, kx, -m)));
+  const uint64_t kx2 = pair(kx, kx);
+  auto exps = [&](const float4& v, uint64_t minus_m, uint64_t& e01, uint64_t& e23) {
+    const float2 a = unpair(fma2(pair(v.x, v.y), kx2, minus_m)), b = unpair(fma2(pair(v.z, v.w), kx2, minus_m));
+    e01 = pair(ex2(a.x), ex2(a.y));
+    e23 = pair(ex2(b.x), ex2(b.y));
   };
   if (!helper) {
-    each([&](int j, float4& v) {
+    each(j_first, std::true_type{}, [&](int j, float4& v) {
       if (CAP) {
         v = tanh_of(v);
         if (!FULL && (j < off || j + 4 > end)) {  // positions outside the row stay -inf
@@ -248,31 +356,40 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
         ms.x = fmaxf(ms.x, m);
       } else {
         const float mn = fmaxf(ms.x, m * kx);
-        if (mn != -INFINITY) ms = make_float2(mn, ms.y * ex2(ms.x - mn) + sum4(v, mn));
+        if (mn != -INFINITY) {
+          uint64_t e01, e23;
+          exps(v, pair(-mn, -mn), e01, e23);
+          const float2 s = unpair(add2(e01, e23));
+          ms = make_float2(mn, ms.y * ex2(ms.x - mn) + (s.x + s.y));
+        }
       }
     });
+    const float m = warp_max_redux(ms.x) * (REGS > 0 ? kx : 1.0f);
     if constexpr (REGS > 0) {
-      ms.x *= kx;
-      if (ms.x != -INFINITY) each([&](int, float4& v) { ms.y += sum4(v, ms.x); });
+      if (m != -INFINITY) {
+        const uint64_t minus_m = pair(-m, -m);
+        uint64_t sum = 0ull;  // a pair of zeros
+        each(j_first, std::false_type{}, [&](int, float4& v) {
+          uint64_t e01, e23;
+          exps(v, minus_m, e01, e23);
+          sum = add2(sum, add2(e01, e23));
+        });
+        const float2 s = unpair(sum);
+        ms.y = s.x + s.y;
+      }
+    } else {
+      ms.y = ms.x == -INFINITY ? 0.0f : ms.y * ex2(ms.x - m);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      ms = join(ms, make_float2(__shfl_xor_sync(0xffffffffu, ms.x, o), __shfl_xor_sync(0xffffffffu, ms.y, o)));
+    ms = make_float2(m, warp_sum(ms.y));
     if (lane == 0) sh.part_w[warp] = ms;
   }
-  auto join_lanes = [&](const float2* v, int n) {  // n <= 8 parts, in a fixed tree
-    float2 x = lane < n ? v[lane] : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-      x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
-    return make_float2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0));
-  };
+  auto part_of = [&](const float2* v, int n) { return lane < n ? v[lane] : make_float2(-INFINITY, 0.0f); };
   // The row's warps meet (the helper is not waited for), and warp 0 sends the CTA's
   // part to every CTA of the cluster; each waits for all of them to arrive.
   if (!helper) {
     named_sync(1, kThreads);
     if (warp == 0) {
-      ms = join_lanes(sh.part_w, kThreads / 32);
+      ms = join8(part_of(sh.part_w, kThreads / 32));
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
       if (lane < CS)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
@@ -296,11 +413,28 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
       return;
     }
   }
-  ms = join_lanes(sh.part, CS);
-  const float xm = ms.x, xs = ms.y;
+  ms = join8(part_of(sh.part, CS));
+  const float xm = ms.x, xs = __shfl_sync(0xffffffffu, ms.y, 0);
 
+  auto store_loss = [&] {  // the helper's
+    const float xlse = logf(xs);
+    float loss = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+      const float lq = q_s[k] - t_lse, q = t_any ? expf(lq) : 0.0f;
+      if (q > 0.0f) {
+        const float t = CAP ? tanh_of(z_s[k]) : z_s[k];
+        loss = fmaf(q, lq - (fmaf(t, kx, -xm) * 0.6931471805599453f - xlse), loss);
+      }
+    }
+    loss = warp_sum(loss);
+    if (lane == 0) p.loss[blockIdx.y] = t_any ? p.tau * p.tau * loss : 0.0f;
+  };
   auto slope = [&](float t) { return CAP ? fmaf(-t, t, 1.0f) : 1.0f; };
   if constexpr (DZ != 0) {
+    const int64_t row = fresh_row();
+    const int rank = fresh_rank(), tid = fresh_tid(), lane = tid & 31;
+    const int off = (int)((reinterpret_cast<uintptr_t>(p.z + row * p.V) >> 2) & 3), end = off + p.V;
+    const int s0 = rank * slice, s1 = min(end, s0 + slice), j_first = s0 + tid * 4;
     const float wp = p.tau * (p.weight ? p.weight[row] : 1.0f) / xs;
     constexpr int ES = DZ == 1 ? 4 : 2;
     uint8_t* dr = static_cast<uint8_t*>(p.dz) + row * V * ES - (int64_t)off * ES;  // position 0
@@ -312,10 +446,16 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
         reinterpret_cast<uint16_t*>(dr)[j] = (uint16_t)Half<DZ == 3>::pack2(v, 0.0f);
     };
     if (!helper) {
-      each([&](int j, float4& v) {
+      each(j_first, std::false_type{}, [&](int j, float4& v) {
         const float4 t = CAP && REGS == 0 ? tanh_of(v) : v;
-        const float4 d = make_float4(ex2(fmaf(t.x, kx, -xm)) * (wp * slope(t.x)), ex2(fmaf(t.y, kx, -xm)) * (wp * slope(t.y)),
-                                     ex2(fmaf(t.z, kx, -xm)) * (wp * slope(t.z)), ex2(fmaf(t.w, kx, -xm)) * (wp * slope(t.w)));
+        uint64_t e01, e23;
+        exps(t, pair(-xm, -xm), e01, e23);
+        auto scaled = [&](uint64_t e, uint64_t u) {  // w tau / sum (1 - u^2) e
+          const uint64_t w2 = pair(wp, wp);
+          return unpair(mul2(e, CAP ? fma2(mul2(u, pair(-wp, -wp)), u, w2) : w2));
+        };
+        const float2 d01 = scaled(e01, pair(t.x, t.y)), d23 = scaled(e23, pair(t.z, t.w));
+        const float4 d = make_float4(d01.x, d01.y, d23.x, d23.y);
         if (vec && (FULL || (j >= off && j + 4 <= end))) {
           if constexpr (DZ == 1)
             __stcs(reinterpret_cast<float4*>(dr + (int64_t)j * 4), d);
@@ -331,49 +471,77 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
       });
       named_arrive(2, kBlock);
     } else {
-      named_sync(2, kBlock);  // the row is stored; the teacher's entries go over it
+      // the entries' gradients, while the row is stored; then they go over it
       const float tlse = t_lse, w = p.tau * (p.weight ? p.weight[row] : 1.0f), inv = 1.0f / xs;
+      const int n = t_any ? n_here : 0;
+      __syncwarp();
+      auto insert = [&](int i) {  // into a table of 2 K slots or more
+        for (int h = i;; ++h) {
+          const int was = atomicCAS(&table[h & (slots - 1)], -1, i);
+          if (was == -1) return;
+          if ((was & ~kTwice) == i) {
+            atomicOr(&table[h & (slots - 1)], kTwice);
+            return;
+          }
+        }
+      };
+      auto is_twice = [&](int i) {
+        int h = i;
+        while ((table[h & (slots - 1)] & ~kTwice) != i) ++h;
+        return (table[h & (slots - 1)] & kTwice) != 0;
+      };
+      if (n > 32) {
+        for (int k = lane; k < slots; k += 32) table[k] = -1;
+        __syncwarp();
+        for (int e = lane; e < n; e += 32) insert(i_s[list[e]]);
+        __syncwarp();
+      }
+      uint32_t mine = 0u;  // the lane's entries that are stored, 32 of them at most
+      for (int e0 = 0, turn = 0; e0 < n; e0 += 32, ++turn) {
+        const bool in = e0 + lane < n;
+        const int k = in ? list[e0 + lane] : 0, i = in ? i_s[k] : -1 - lane;
+        float q = in ? expf(q_s[k] - tlse) : 0.0f;
+        bool first = in;
+        const bool twice = n > 32 ? in && is_twice(i) : (__match_any_sync(0xffffffffu, i) & ~(1u << lane)) != 0u;
+        // an index given more than once: the sum over its entries, stored by the first
+        for (uint32_t bal = __ballot_sync(0xffffffffu, twice); bal != 0u; bal &= bal - 1u) {
+          const int s = __ffs(bal) - 1, is = __shfl_sync(0xffffffffu, i, s);
+          float sum = 0.0f;
+          int least = n;
+          for (int f = lane; f < n; f += 32)
+            if (i_s[list[f]] == is) {
+              sum += expf(q_s[list[f]] - tlse);
+              least = min(least, f);
+            }
+          sum = warp_sum(sum);
+          least = __reduce_min_sync(0xffffffffu, least);
+          if (lane == s) {
+            q = sum;
+            first = least == e0 + lane;
+          }
+        }
+        if (in) {
+          const float t = CAP ? tanh_of(z_s[k]) : z_s[k];
+          g_s[e0 + lane] = (ex2(fmaf(t, kx, -xm)) * inv - q) * w * slope(t);
+        }
+        if (first) mine |= 1u << turn;
+      }
+      if (rank == 0) store_loss();
+      named_sync(2, kBlock);
+      for (int e = lane; mine != 0u; e += 32, mine >>= 1)
+        if (mine & 1u) store1(off + i_s[list[e]], g_s[e]);
       if (!t_any)  // no entry: no gradient
         for (int j = max(s0, off) + lane; j < s1; j += 32) store1(j, 0.0f);
-      const bool twice = t_twice;
-      for (int k = lane; k < K && t_any; k += 32) {
-        const int i = i_s[k];
-        if (i < 0 || off + i < s0 || off + i >= s1) continue;
-        float q = expf(q_s[k] - tlse);
-        bool first = true;
-        if (twice) {  // its first entry stores for all
-          q = 0.0f;
-          for (int j = 0; j < K; ++j)
-            if (i_s[j] == i) {
-              first = first && j >= k;
-              q += expf(q_s[j] - tlse);
-            }
-        }
-        const float t = CAP ? tanh_of(z_s[k]) : z_s[k];
-        if (first) store1(off + i, (ex2(fmaf(t, kx, -xm)) * inv - q) * w * slope(t));
-      }
     }
-  }
-  if (helper && rank == 0) {
-    const bool any = t_any;
-    const float tlse = t_lse, xlse = logf(xs);
-    float loss = 0.0f;
-    for (int k = lane; k < K; k += 32) {
-      const float lq = q_s[k] - tlse, q = any ? expf(lq) : 0.0f;
-      if (q > 0.0f) {
-        const float t = CAP ? tanh_of(z_s[k]) : z_s[k];
-        loss = fmaf(q, lq - (fmaf(t, kx, -xm) * 0.6931471805599453f - xlse), loss);
-      }
-    }
-    loss = warp_sum(loss);
-    if (lane == 0) p.loss[row] = any ? p.tau * p.tau * loss : 0.0f;
+  } else {
+    if (helper && rank == 0) store_loss();
   }
 }
 
 template <int DZ, bool CAP, int REGS>
-__global__ void __launch_bounds__(kBlock, REGS == 8 ? 4 : 1)
+__global__ void __launch_bounds__(kBlock, resident(DZ, REGS))
     distill_kernel(const DistillParams p, int slice, int slots) {
-  extern __shared__ float q_s[];
+  extern __shared__ __align__(16) float mem[];
   __shared__ Shared sh;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh.bar), 1);
@@ -385,9 +553,9 @@ __global__ void __launch_bounds__(kBlock, REGS == 8 ? 4 : 1)
   const int off = (int)((reinterpret_cast<uintptr_t>(p.z + (int64_t)blockIdx.y * p.V) >> 2) & 3);
   const int s0 = blockIdx.x * slice;
   if (REGS == 8 && s0 >= off && s0 + REGS * 4 * kThreads <= off + p.V)
-    distill_part<DZ, CAP, REGS, true>(p, slice, slots, q_s, sh);
+    distill_part<DZ, CAP, REGS, true>(p, slice, slots, mem, sh);
   else
-    distill_part<DZ, CAP, REGS, false>(p, slice, slots, q_s, sh);
+    distill_part<DZ, CAP, REGS, false>(p, slice, slots, mem, sh);
 }
 
 template <int DZ, bool CAP, int REGS>
@@ -406,7 +574,7 @@ nc_status launch_r(const DistillParams& p, int M, int cs, int slice, cudaStream_
     cfg.blockDim = dim3(kBlock);
     int slots = 2;
     while (slots < 2 * p.K) slots *= 2;
-    cfg.dynamicSmemBytes = (size_t)(3 * p.K + slots) * 4;
+    cfg.dynamicSmemBytes = (size_t)((REGS - held(DZ, REGS)) * kThreads * 4 + 5 * p.K + slots) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;

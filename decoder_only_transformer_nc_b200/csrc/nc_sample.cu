@@ -16,6 +16,14 @@
 // with fp32 weights, whose sums carry a bound of their error: where no border
 // (of top-p's share, of min-p, of the token's own interval) lies within it, the
 // integers would give the same token; only else are they computed.
+//
+// What bounds it: up to some hundred rows, latency (passes of a row that end at a
+// barrier, and code that is met for the first time: a row of 32768 logits, top-k 50
+// and top-p 0.95, takes 14 us, 0.02 us of them at the copy rate); from there, the
+// instructions of a pass.  1024 rows of 32749 logits, one pass: 58 us in a graph for
+// 134 MB (2.3 TB/s, 35 % of a copy); two waves of four rows an SM, with the search of the token's
+// segment behind each row.  The same with top-p 0.95, whose cut lies among thousands of
+// tokens (a histogram and a pass more): 230 us, a row alone 36 us.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -412,8 +420,8 @@ struct Filter {
 };
 
 // The code of the last token that top-k and top-p keep, for any row: bisection
-// over the keys, a pass of the row each.  For rows whose cut falls among more
-// more tokens of one bin than the block has threads (heavy ties, logits spread over hundreds).
+// over the keys, a pass of the row each.  For rows whose cut falls among more tokens
+// of one bin than the block has threads (heavy ties, logits spread over hundreds).
 template <int NT>
 __device__ __noinline__ uint64_t cut_by_bisection(const Row r, const Filter f, const Expo weight, Smem<NT>& sm) {
   const uint32_t kmax = key_of(weight.mx);

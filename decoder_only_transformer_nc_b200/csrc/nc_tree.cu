@@ -78,7 +78,11 @@ __global__ void __launch_bounds__(kMaxNodes) tree_mask_kernel(const int32_t* __r
 // the window's first on, then the drafted ones -- are split over the CTAs of a
 // cluster, which merge their partial results through distributed shared
 // memory: one launch, no workspace, a fixed order of sums.
-// K/V tiles arrive by 16-byte asynchronous copies, kStages deep.  The products
+// K/V tiles arrive by 16-byte asynchronous copies, kStages deep.  What is left of
+// its time is latency, not bytes: 8 us (in a graph) for 4 nodes over 300 positions of
+// 10 heads of 128, whose K/V takes 0.24 us to read; 17 us for 16 rows of 27 nodes, 12
+// heads of 64 and a window of 512, 27 MB or 4.2 us (tensor pipe 10 %, DRAM 16 %: three or
+// four tiles a CTA, each of them waited for at a barrier).  The products
 // run on m16n8k16 with fp32 accumulation; P enters P V in the 16-bit format of
 // the inputs, as in the other attention kernels of the library.
 constexpr int kTK = 64;      // keys per tile
@@ -383,7 +387,9 @@ nc_status tree_attn_rows(const TreeAttnParams& p, int B, cudaStream_t stream) {
 // its first child whose drafted token is the token sampled at that node.  Every
 // CTA walks the path of its row by itself (a warp, up to four nodes a lane; a
 // step is a compare and a ballot), so the copies of a layer wait for no other
-// launch; the CTAs of layer 0 also write the path.
+// launch; the CTAs of layer 0 also write the path.  The walk and the launch are all
+// there is to it: 3.4 us for a row of 8 nodes and 20 layers, 5.0 us for 32 rows of 64
+// nodes and 26 layers, whose 17 MB take 2.6 us.
 __global__ void __launch_bounds__(256) tree_accept_kernel(
     const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents, const uint32_t* __restrict__ mask,
     const int32_t* __restrict__ sampled, const int32_t* __restrict__ lens, const uint4* __restrict__ kv,

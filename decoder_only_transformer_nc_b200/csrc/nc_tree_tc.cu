@@ -28,6 +28,14 @@
 // memory: S_0, S_1 (128 columns each; P replaces the first half in 16 bits),
 // O_0, O_1 (D columns each).  O is rescaled only when the running maximum grows
 // by more than 2^8, as in the other attention kernels.
+// Measured, in a graph: 32 rows of 64 nodes, 16 heads on 4, 3000 to 8100 positions
+// of 128: 112 us for 385 MB and 93 GFLOP (59 us at the copy rate, 57 us at the tensor
+// rate, which no overlap takes below the larger): 3.4 TB/s and 830 TFLOP/s.  The
+// tensor pipe is 49 % busy, the exponentials' 50 %; the rest is the chain of one
+// stream's tile (S, maximum and weights, P, P V), which two streams cover in part:
+// a third would need more tensor memory than 512 columns hold.  8 rows of 32 nodes,
+// 900 to 1990 positions: 20 us for 26 MB; some 10 us are start, plan, first loads and
+// the merge.
 // Every wait is bounded; on timeout the CTA records NC_DEV_TIMEOUT, lets its
 // copies and products land, frees its tensor memory and exits.
 #include <cuda.h>

@@ -678,9 +678,9 @@ nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const ui
  * -inf.  The largest logit weighs 1 also where it is +inf.  logprob may be NULL.
  * The token is that of weights rounded to an absolute unit of V / 2^62 (2^-47 at
  * V <= 32768; smaller ones count as 0) and exact sums, the same run to run.
- * logprob may come from fp32 weights: the mass in it is within 3e-7 + 4.5e-8
- * |log2 w| of each weight, relative (a few 1e-8 in practice).  A row whose copy to
- * the SM does not arrive in time gives token -1 and logprob NaN.
+ * logprob may come from fp32 weights: the mass in it is within 4.5e-7 of each
+ * weight, relative (a few 1e-8 in practice).  A row whose copy to the SM does not
+ * arrive in time gives token -1 and logprob NaN.
  * 1 <= V <= 2^24. */
 nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, const float* temperature,
                     const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, float* logprob,

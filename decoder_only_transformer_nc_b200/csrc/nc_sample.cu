@@ -97,13 +97,12 @@ __device__ __forceinline__ double wide_weight(float x) {
 // logprob of a token that is nearly certain).
 struct Sum {
   double v = 0.0;
-  __device__ __forceinline__ float add(float a, float b, float c, float d, float big = 1.0f) {
+  __device__ __forceinline__ void add(float a, float b, float c, float d, float big = 1.0f) {
     const float x = (a + b) + (c + d);
     if (x < big)
       v += wide_weight(x);
     else
       v += (wide_weight(a) + wide_weight(b)) + (wide_weight(c) + wide_weight(d));
-    return x;
   }
 };
 
@@ -866,7 +865,6 @@ __device__ __noinline__ int pick_plain(const Row r, float u, float T, double c, 
       return wide_weight(wf.scaled(l));
   };
   Sum sum;
-  float most = 0.0f;
 #pragma unroll 1
   for (int j = j0; j - lane * 4 < r.seg1;) {
     float4 x[U];
@@ -880,10 +878,11 @@ __device__ __noinline__ int pick_plain(const Row r, float u, float T, double c, 
       if constexpr (FINE)
         sum.v += (weight(x[e].x) + weight(x[e].y)) + (weight(x[e].z) + weight(x[e].w));
       else
-        most = fmaxf(most, sum.add(wf.scaled(x[e].x), wf.scaled(x[e].y), wf.scaled(x[e].z), wf.scaled(x[e].w), kBig));
+        sum.add(wf.scaled(x[e].x), wf.scaled(x[e].y), wf.scaled(x[e].z), wf.scaled(x[e].w), kBig);
     }
   }
   double mass = sum.v;
+  const bool above = mx * (float)c > n0;  // a weight above 1 (its bits may be anything)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mass += __shfl_xor_sync(0xffffffffu, mass, o);
@@ -894,7 +893,7 @@ __device__ __noinline__ int pick_plain(const Row r, float u, float T, double c, 
     *reinterpret_cast<double*>(&sm.seg[warp]) = mass;
     sm.redf[0][warp] = mx;
   }
-  if (__syncthreads_or(most > 1.0f)) return -1;
+  if (__syncthreads_or(above)) return -1;
   double total;
   const int pick = locate<NT, false>(
       r, sm, u, total, [&](int, float l) { return l > -INFINITY ? weight(l) : 0.0; },

@@ -364,6 +364,24 @@ def test_sample_logits_of_any_spread(gpu, scale):
             _check_sample(l, u, tok, lp, np.full(M, T), **kw)
 
 
+@pytest.mark.parametrize("M", [30, 180])  # one row an SM, and several
+def test_sample_maxima_far_above_the_rest(gpu, M):
+    """One or a few tokens anywhere in the row, from e^2 to e^5000 (and infinitely) above the others."""
+    V = 32768
+    rng = np.random.default_rng(M)
+    l = rng.standard_normal((M, V)).astype(np.float32)
+    for m in range(M):
+        h = [2, 5, 8, 9, 12, 60, 80, 88, 90, 120, 176, 178, 200, 300, 1000, 5000, np.inf][m % 17]
+        at = rng.integers(0, V, 1 + m % 3)
+        l[m, at] += np.float32(h)
+        if m % 5 == 0:  # and all the first of every part far below
+            for s in range(0, V, 2048):
+                l[m, s:s + 512] -= 500
+    u = rng.random(M).astype(np.float32)
+    tok, lp = _sample(gpu, l, u)
+    _check_sample(l, u, tok, lp)
+
+
 @pytest.mark.parametrize("M", [24, 200])  # one row an SM, and several
 @pytest.mark.parametrize("how", ["plain", "p", "kp", "m"])
 def test_sample_at_the_borders(gpu, M, how):

@@ -752,6 +752,18 @@ def loss_mean(token_loss, targets, V, loss, stream=None):
 
 # ---------------------------------------------------------------- drafted trees, sampling, distillation
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported at the first call (the statement costs a fifth of a us in each)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _arg(where, name, t, dtype, shape, dev):
     """Checks one tensor argument (dev: its device's index, -1 for the host);
     returns its address (0 for an absent one)."""
@@ -766,6 +778,20 @@ def _arg(where, name, t, dtype, shape, dev):
     if not t.is_contiguous():
         raise NcError(1, f"{where}: {name} is not contiguous")
     raise NcError(1, f"{where}: {name} is on {t.device}, the first tensor is on another device")
+
+
+def _same(where, dev, dtype, shape, names, *tensors):
+    """Addresses of tensors of one type and shape (names: theirs, with blanks
+    between).  The short calls of these operators take the GPU less time than
+    their checks take the host, so the common case is one expression a tensor."""
+    out = []
+    for t in tensors:
+        if (t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            out.append(_arg(where, names.split()[len(out)], t, dtype, shape, dev))
+    return out
 
 
 def _status_word(where, t, dev):
@@ -783,9 +809,9 @@ def _status_word(where, t, dev):
 def _launch(where, dev, stream, fn, *args):
     """Calls a library function on device ``dev`` (an index), on ``stream`` (of
     that device) or the device's current stream."""
-    import torch
     if dev < 0:
         raise NcError(8, f"{where}: the tensors are not on a CUDA device")
+    torch = _torch()
     if stream is None:
         # the public torch.cuda.current_stream builds a Stream object: 2 us, half a launch
         raw = torch._C._cuda_getCurrentRawStream(dev)
@@ -836,7 +862,7 @@ def tree_attention(q, kv, cache, lens, mask, out, window=0, workspace=None, stat
     [B, N, ceil(N / 32)] int32 (tree_mask).  workspace: a uint8 tensor of
     nc_tree_attention_workspace_bytes bytes (None: a new one).  status: a device
     status word (int32 or uint8 tensor) or None."""
-    import torch
+    torch = _torch()
     where = "tree_attention"
     if q.dim() != 4 or cache.dim() != 5:
         raise NcError(3, f"{where}: q {tuple(q.shape)}, cache {tuple(cache.shape)}")
@@ -870,7 +896,7 @@ def sample(logits, u, tokens, logprob=None, temperature=None, top_k=None, top_p=
     """One token a row from logits [M, V] fp32 (rows may be strided) and uniform
     numbers u [M] fp32 into tokens [M] int32 and logprob [M] fp32 (nc_sample).
     temperature, top_p, min_p: [M] fp32 or None; top_k: [M] int32 or None."""
-    import torch
+    torch = _torch()
     where = "sample"
     if logits.dim() != 2:
         raise NcError(3, f"{where}: logits {tuple(logits.shape)}")
@@ -883,12 +909,12 @@ def sample(logits, u, tokens, logprob=None, temperature=None, top_k=None, top_p=
     dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
     if u is None or tokens is None:
         raise NcError(1, f"{where}: u and tokens are needed")
-    a = (_arg(where, "u", u, f32, (M,), dev), _arg(where, "temperature", temperature, f32, (M,), dev),
-         _arg(where, "top_k", top_k, i32, (M,), dev), _arg(where, "top_p", top_p, f32, (M,), dev),
-         _arg(where, "min_p", min_p, f32, (M,), dev), _arg(where, "tokens", tokens, i32, (M,), dev),
-         _arg(where, "logprob", logprob, f32, (M,), dev))
+    m = (M,)
+    up, tp, pp, mp, lp = _same(where, dev, f32, m, "u temperature top_p min_p logprob", u, temperature, top_p, min_p,
+                               logprob)
+    kp, op = _same(where, dev, i32, m, "top_k tokens", top_k, tokens)
     if M:
-        _launch(where, dev, stream, lib().nc_sample, logits.data_ptr(), ld, *a, M, V)
+        _launch(where, dev, stream, lib().nc_sample, logits.data_ptr(), ld, up, tp, kp, pp, mp, op, lp, M, V)
 
 
 def tree_accept(tokens, parents, mask, sampled, lens, kv, cache, path, count, next, lens_out, stream=None):
@@ -898,22 +924,20 @@ def tree_accept(tokens, parents, mask, sampled, lens, kv, cache, path, count, ne
     tokens, parents, sampled, path [B, N] int32, mask [B, N, ceil(N / 32)]
     int32, lens, count, next, lens_out [B] int32; kv [L, B, N, 2, Hkv, D] and
     cache [L, B, T_max, 2, Hkv, D] fp16 or bf16."""
-    import torch
     where = "tree_accept"
     if kv.dim() != 6 or cache.dim() != 6:
         raise NcError(3, f"{where}: kv {tuple(kv.shape)}, cache {tuple(cache.shape)}")
     L, B, N, _, Hkv, D = kv.shape
     T_max = cache.shape[2]
     _dt(kv)
-    dev, i32, bn, b1 = kv.get_device(), torch.int32, (B, N), (B,)
-    a = (_arg(where, "tokens", tokens, i32, bn, dev), _arg(where, "parents", parents, i32, bn, dev),
-         _arg(where, "mask", mask, i32, (B, N, (N + 31) // 32), dev), _arg(where, "sampled", sampled, i32, bn, dev),
-         _arg(where, "lens", lens, i32, b1, dev), _arg(where, "kv", kv, kv.dtype, (L, B, N, 2, Hkv, D), dev),
-         _arg(where, "cache", cache, kv.dtype, (L, B, T_max, 2, Hkv, D), dev),
-         _arg(where, "path", path, i32, bn, dev), _arg(where, "count", count, i32, b1, dev),
-         _arg(where, "next", next, i32, b1, dev), _arg(where, "lens_out", lens_out, i32, b1, dev))
+    dev, i32, dt = kv.get_device(), _torch().int32, kv.dtype
+    tp, pp, sp, ap = _same(where, dev, i32, (B, N), "tokens parents sampled path", tokens, parents, sampled, path)
+    lp, cp, xp, op = _same(where, dev, i32, (B,), "lens count next lens_out", lens, count, next, lens_out)
+    mp = _arg(where, "mask", mask, i32, (B, N, (N + 31) // 32), dev)
+    kp, hp = _arg(where, "kv", kv, dt, (L, B, N, 2, Hkv, D), dev), _arg(where, "cache", cache, dt, (L, B, T_max, 2, Hkv, D), dev)
     if B:
-        _launch(where, dev, stream, lib().nc_tree_accept, *a, B, N, L, Hkv, D, T_max)
+        _launch(where, dev, stream, lib().nc_tree_accept, tp, pp, mp, sp, lp, kp, hp, ap, cp, xp, op, B, N, L, Hkv, D,
+                T_max)
 
 
 def distill_topk(z, teacher_idx, teacher_logits, token_loss, dz=None, tau=1.0, cap=15.0, row_weight=None, status=None,
@@ -924,7 +948,7 @@ def distill_topk(z, teacher_idx, teacher_logits, token_loss, dz=None, tau=1.0, c
     z [M, V] fp32; teacher_idx [M, K] int32 (-1: unused), teacher_logits [M, K],
     token_loss [M] and row_weight [M] fp32; dz [M, V] fp32, bf16 or fp16; status:
     a device status word (int32 or uint8 tensor) or None."""
-    import torch
+    torch = _torch()
     where = "distill_topk"
     if z.dim() != 2 or teacher_idx.dim() != 2:
         raise NcError(3, f"{where}: z {tuple(z.shape)}, teacher_idx {tuple(teacher_idx.shape)}")

@@ -184,8 +184,10 @@ __device__ __forceinline__ float2 join8(float2 v) {
 // takes longer than the row from K = 128 or so (4096 rows without a gradient: 117 us
 // at K = 64, 330 at 512).
 // REGS = 0: longer rows, one CTA, read again from L2 for each use.
-// Groups of four start at 16-byte boundaries of z's row (the ends and a dz that is
-// not aligned alike go by single elements).
+// Groups of four start at 16-byte boundaries of z's row; the row's ends and a dz that
+// is not aligned alike go by single elements.  2048 rows of 32767 logits without a
+// gradient take 86 us (106 while every group was tested for the ends), those of 32768
+// 61: the odd ones start anywhere, which takes a fifth CTA a row.
 // DZ: 0 none, 1 fp32, 2 bf16, 3 fp16
 struct Shared {
   float2 part[8], part_w[kThreads / 32];
@@ -253,32 +255,33 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
   const int s0 = rank * slice, s1 = min(end, s0 + slice);  // this CTA's positions
   const Tanh& tanh_of = p.tanh_of;
   const float kx = p.kx;
-  auto load = [&](int j) -> float4 {
-    if (FULL || (j >= off && j + 4 <= end)) return __ldcs(reinterpret_cast<const float4*>(z + j));
-    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (j >= off && j < end) v.x = z[j];
-    if (j + 1 >= off && j + 1 < end) v.y = z[j + 1];
-    if (j + 2 >= off && j + 2 < end) v.z = z[j + 2];
-    if (j + 3 >= off && j + 3 < end) v.w = z[j + 3];
-    return v;
-  };
+  auto load = [&](int j) { return __ldcs(reinterpret_cast<const float4*>(z + j)); };
   constexpr int STEP = kThreads * 4;
   const int j_first = s0 + tid * 4;
-  // groups of this thread (0 or less: none)
-  const int nr = warp == kThreads / 32 ? 0 : (s1 - j_first + STEP - 1) / STEP;
+  // Whole groups of four from position `lo` on; this thread has the first nr (0 or
+  // less: none) but for one before lo.  What is left of the row's ends, up to three
+  // logits each, is dealt to the first six threads, one each (`edge` at je).
+  const int lo = off > 0 ? 4 : 0;
+  const int nr = warp == kThreads / 32 ? 0 : (min(s0 + slice, end & ~3) - j_first + STEP - 1) / STEP;
+  int je = -1;
+  float edge = -INFINITY;
+  if (!FULL && tid < 6) {
+    const int tail = end & ~3;
+    if (tid < 3) {
+      if (s0 == 0 && off > 0 && off + tid < min(4, end)) je = off + tid;
+    } else if (tail >= lo && tail >= s0 && tail < s0 + slice && tail + tid - 3 < end) {
+      je = tail + tid - 3;
+    }
+    if (je >= 0) edge = z[je];
+  }
   float4 keep[HELD > 0 ? HELD : 1];
   if constexpr (REGS > 0) {
 #pragma unroll
-    for (int r = HELD; r < REGS; ++r) {
-      if (FULL) {
-        if (warp < kThreads / 32) cp_async16(own + (r - HELD) * kThreads, z + j_first + r * STEP);
-      } else if (r < nr) {
-        own[(r - HELD) * kThreads] = load(j_first + r * STEP);
-      }
-    }
+    for (int r = HELD; r < REGS; ++r)
+      if (FULL ? warp < kThreads / 32 : r < nr) cp_async16(own + (r - HELD) * kThreads, z + j_first + r * STEP);
 #pragma unroll
     for (int r = 0; r < HELD; ++r)
-      if (FULL ? warp < kThreads / 32 : r < nr) keep[r] = load(j_first + r * STEP);
+      if (FULL ? warp < kThreads / 32 : r < nr && (r > 0 || j_first >= lo)) keep[r] = load(j_first + r * STEP);
   }
   // f(position, four values); WRITE: f changes them
   auto each = [&](int j_first, auto write, auto f) {
@@ -286,8 +289,8 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
       constexpr bool WRITE = decltype(write)::value;
 #pragma unroll
       for (int r = 0; r < HELD; ++r)
-        if (FULL || r < nr) f(j_first + r * STEP, keep[r]);
-      if (FULL && WRITE && REGS > HELD) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (FULL || (r < nr && (r > 0 || j_first >= lo))) f(j_first + r * STEP, keep[r]);
+      if (WRITE && REGS > HELD) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
       for (int r = HELD; r < REGS; ++r)
         if (FULL || r < nr) {
@@ -298,6 +301,7 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
     } else {
 #pragma unroll 1
       for (int j = j_first, r = 0; r < nr; ++r, j += STEP) {
+        if (j < lo) continue;
         float4 v = load(j);
         f(j, v);
       }
@@ -351,16 +355,8 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
     e23 = pair(ex2(b.x), ex2(b.y));
   };
   if (!helper) {
-    each(j_first, std::true_type{}, [&](int j, float4& v) {
-      if (CAP) {
-        v = tanh_of(v);
-        if (!FULL && (j < off || j + 4 > end)) {  // positions outside the row stay -inf
-          if (j < off || j >= end) v.x = -INFINITY;
-          if (j + 1 < off || j + 1 >= end) v.y = -INFINITY;
-          if (j + 2 < off || j + 2 >= end) v.z = -INFINITY;
-          if (j + 3 < off || j + 3 >= end) v.w = -INFINITY;
-        }
-      }
+    each(j_first, std::true_type{}, [&](int, float4& v) {
+      if (CAP) v = tanh_of(v);
       const float m = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
       if (REGS > 0) {
         ms.x = fmaxf(ms.x, m);
@@ -374,6 +370,15 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
         }
       }
     });
+    if (!FULL && je >= 0) {
+      if (CAP) edge = tanh_of(edge);
+      if (REGS > 0) {
+        ms.x = fmaxf(ms.x, edge);
+      } else {
+        const float mn = fmaxf(ms.x, edge * kx);
+        if (mn != -INFINITY) ms = make_float2(mn, ms.y * ex2(ms.x - mn) + ex2(fmaf(edge, kx, -mn)));
+      }
+    }
     const float m = warp_max_redux(ms.x) * (REGS > 0 ? kx : 1.0f);
     if constexpr (REGS > 0) {
       if (m != -INFINITY) {
@@ -386,6 +391,7 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
         });
         const float2 s = unpair(sum);
         ms.y = s.x + s.y;
+        if (!FULL && je >= 0) ms.y += ex2(fmaf(edge, kx, -m));
       }
     } else {
       ms.y = ms.x == -INFINITY ? 0.0f : ms.y * ex2(ms.x - m);
@@ -466,19 +472,20 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
         };
         const float2 d01 = scaled(e01, pair(t.x, t.y)), d23 = scaled(e23, pair(t.z, t.w));
         const float4 d = make_float4(d01.x, d01.y, d23.x, d23.y);
-        if (vec && (FULL || (j >= off && j + 4 <= end))) {
+        if (vec) {
           if constexpr (DZ == 1)
             __stcs(reinterpret_cast<float4*>(dr + (int64_t)j * 4), d);
           else
             __stcs(reinterpret_cast<uint2*>(dr + (int64_t)j * 2),
                    make_uint2(Half<DZ == 3>::pack2(d.x, d.y), Half<DZ == 3>::pack2(d.z, d.w)));
         } else {
-          if (j >= off && j < end) store1(j, d.x);
-          if (j + 1 >= off && j + 1 < end) store1(j + 1, d.y);
-          if (j + 2 >= off && j + 2 < end) store1(j + 2, d.z);
-          if (j + 3 >= off && j + 3 < end) store1(j + 3, d.w);
+          store1(j, d.x);
+          store1(j + 1, d.y);
+          store1(j + 2, d.z);
+          store1(j + 3, d.w);
         }
       });
+      if (!FULL && je >= 0) store1(je, ex2(fmaf(edge, kx, -xm)) * (wp * slope(edge)));
       named_arrive(2, kBlock);
     } else {
       // the entries' gradients, while the row is stored; then they go over it

@@ -27,7 +27,8 @@
 // for the other: PV_w(i - 1), S_w(i) are issued in turn for w = 0, 1.  Tensor
 // memory: S_0, S_1 (128 columns each; P replaces the first half in 16 bits),
 // O_0, O_1 (D columns each).  O is rescaled only when the running maximum grows
-// by more than 2^8, as in the other attention kernels.
+// by more than 2^8, as in the other attention kernels.  P enters P V in 16 bits (the
+// row's sum keeps it in fp32), times 2^kLift (see there).
 // Measured, in a graph: 32 rows of 64 nodes, 16 heads on 4, 3000 to 8100 positions
 // of 128: 112 us for 385 MB and 93 GFLOP (59 us at the copy rate, 57 us at the tensor
 // rate, which no overlap takes below the larger): 3.4 TB/s and 830 TFLOP/s.  The
@@ -55,6 +56,10 @@ constexpr int NUM_THREADS = 64 + 256;
 constexpr int ATOM = 128 * 128;  // bytes of one [128 rows][64 x 16-bit] swizzle tile
 constexpr int kMaxB = 1024;      // rows whose tile counts a CTA keeps
 constexpr float kRescaleLog2 = 8.0f;
+// Weights are held times 2^7: with the 2^8 that they may grow they stay under fp16's
+// 65504, and one is lost below 2^-32 of the largest, not 2^-25: 2^22 keys of those weigh
+// no more than half a rounding step of fp16 (at 2^-25 they would weigh an eighth).
+constexpr float kLift = 7.0f;
 
 template <int D>
 struct Geo {
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t pk[BKV / 2];
           float mx = -INFINITY, lt = 0.0f;
           auto weigh = [&](float m) {
-            const float ms = m == -INFINITY ? 0.0f : m * p.scale_log2;
+            const float ms = (m == -INFINITY ? 0.0f : m * p.scale_log2) - kLift;
             // two at a time (packed fp32 multiply-adds and sums)
             const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), ms2 = pack_f32x2(-ms, -ms);
             uint64_t ls4[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of zeros

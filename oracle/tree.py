@@ -114,3 +114,33 @@ def distill_row(z, idx, t, tau, cap, weight=1.0):
     if cap > 0:
         d *= 1 - (l / cap) ** 2
     return loss, d
+
+
+def sample_units(l, u, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, logprob) of one row as nc_sample defines it: weights rounded to units of 2^-sh, sums of
+    whole numbers.  u, top_p and min_p as exact fractions; few distinct logits (each costs a 60-digit exponential)."""
+    from decimal import Decimal, getcontext
+    from fractions import Fraction
+    getcontext().prec = 60
+    V = len(l)
+    sh = min(62 - (V - 1).bit_length(), 51)
+    top = l.max()
+    vals, which = np.unique(l, return_inverse=True)
+    units = [int((((Decimal(float(v)) - Decimal(float(top))) / Decimal(T)).exp() * (1 << sh)).to_integral_value()) for v in vals]
+    w = np.array(units, np.int64)[which]  # sums stay under 2^63
+    order = np.lexsort((np.arange(V), -l))
+    if 0 < top_k < V:
+        order = order[:top_k]
+    if top_p < 1:
+        c = np.cumsum(w[order])
+        want = Fraction(max(top_p, 0.0)) * int(c[-1])
+        order = order[:max(1, int(np.searchsorted(c - w[order], -(-want.numerator // want.denominator), side="left")))]
+    if min_p > 0:
+        least = Fraction(min(min_p, 1.0)) * (1 << sh)
+        order = order[w[order] >= -(-least.numerator // least.denominator)]
+    kept = np.sort(order)
+    kept = kept[w[kept] > 0]
+    c = np.cumsum(w[kept])
+    x = Fraction(min(max(u, 0.0), 1.0)) * int(c[-1])
+    i = min(int(np.searchsorted(c, x.numerator // x.denominator, side="right")), len(kept) - 1)
+    return int(kept[i]), float(l[kept[i]] - top) / T - math.log(int(c[-1])) + sh * math.log(2)

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int r = (int)(quarter * 32 + lane);  // this thread's row of the tile
     const uint32_t lane_off = (quarter * 32u) << 16;
     const uint32_t scol = tmem + lane_off + w * BKV, ocol = tmem + lane_off + O_COL;
-    const float thresh = kRescaleLog2 / p.scale_log2;
+    const float lift = kLift / p.scale_log2, thresh = kRescaleLog2 / p.scale_log2 + lift;
     const int W = (p.N + 31) / 32;
     int gt = 0, n = 0, gs = 0, go[2] = {0, 0};
     bool ok = true;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       const bool live_warp = __any_sync(0xffffffffu, depth >= 0);
       const int tmin = depth >= 0 ? rw.len + depth - p.win + 1 : 0;  // first visible position (unused rows: any)
-      float m_used = -INFINITY, l = 0.0f;
+      float m_used = -INFINITY, l = 0.0f;  // m_used: a maximum so far, less lift
       bool first = true;
       for (int j = sg.two ? 0 : w; j < sg.n; j += sg.two ? 1 : 2) {
         if (__any_sync(0xffffffffu, !mbar_wait(smem_u32(&bar->s_full[w]), (uint32_t)gs & 1, ctl))) {
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t pk[BKV / 2];
           float mx = -INFINITY, lt = 0.0f;
           auto weigh = [&](float m) {
-            const float ms = (m == -INFINITY ? 0.0f : m * p.scale_log2) - kLift;
+            const float ms = m == -INFINITY ? 0.0f : m * p.scale_log2;
             // two at a time (packed fp32 multiply-adds and sums)
             const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), ms2 = pack_f32x2(-ms, -ms);
             uint64_t ls4[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of zeros
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(rr[e]));
             }
-            m_used = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            m_used = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) - lift;
           }
 #pragma unroll 1
           for (;;) {
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const bool need = mx > m_used + thresh || (m_used == -INFINITY && mx != -INFINITY);
             if (!__any_sync(0xffffffffu, need)) break;
             // the stream's last P V came before this S, so it has landed
-            const float alpha = need && m_used != -INFINITY ? ex2f((m_used - mx) * p.scale_log2) : 1.0f;
+            const float alpha = need && m_used != -INFINITY ? ex2f((m_used - (mx - lift)) * p.scale_log2) : 1.0f;
             if (!first) {
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               tmem_wait_st();
             }
             l *= alpha;
-            if (need) m_used = mx;
+            if (need) m_used = mx - lift;
           }
           l += lt;
 #pragma unroll

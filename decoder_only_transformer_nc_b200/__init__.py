@@ -388,8 +388,9 @@ class Session:
         self._tree = None
 
     def _used_on(self, stream, *tensors):
-        """The session's own tensors may be dropped while a call on another stream than
-        the one they were made on still runs."""
+        """Tensors that the session holds (its own, and a tree's tokens and parents until it
+        is accepted or dropped), and samples handed over as a temporary, may be freed while a
+        call on another stream than the one they were made on still runs."""
         import torch
         s = stream if stream is not None else torch.cuda.current_stream(self.buffer.device)
         for t in tensors:
@@ -435,7 +436,7 @@ class Session:
                 logits = torch.empty((self.B, N, cfg.vocab), dtype=torch.float32, device=device)
         lp = _arg(where, "logits", logits, torch.float32, (self.B, N, cfg.vocab), dev)
         self._tree = None
-        self._used_on(stream, lens, self._tree_ws)
+        self._used_on(stream, lens, self._tree_ws, tokens, parents)
         _launch(where, dev, stream, lib().nc_decode_tree, ctypes.byref(cfg), ctypes.byref(self.model.weights), tp, pp,
                 lens.data_ptr(), self.B, N, lp, self.buffer.data_ptr(), self.buffer.numel(), self.T_max,
                 self._tree_ws.data_ptr(), self._tree_ws.numel())
@@ -458,7 +459,7 @@ class Session:
         with _allocate_on(stream):
             path = torch.empty((self.B, N), dtype=torch.int32, device=device)
             count, nxt, lens_out = (torch.empty(self.B, dtype=torch.int32, device=device) for _ in range(3))
-        self._used_on(stream, lens, self._tree_ws)
+        self._used_on(stream, lens, self._tree_ws, tokens, parents, sampled)
         _launch(where, dev, stream, lib().nc_accept_tree, ctypes.byref(self.model.cfg), tokens.data_ptr(),
                 parents.data_ptr(), sp, lens.data_ptr(), self.B, N, path.data_ptr(), count.data_ptr(), nxt.data_ptr(),
                 lens_out.data_ptr(), self.buffer.data_ptr(), self.buffer.numel(), self.T_max,

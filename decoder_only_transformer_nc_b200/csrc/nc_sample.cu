@@ -596,7 +596,7 @@ __device__ __noinline__ bool pick_from_list(int n, int k, float tp, int64_t z_lo
 // segment, hold every kept one: one pass
 // lists them in index order and sums the others' mass; the rest happens in
 // registers, kPer tokens a thread with integer weights.  The cuts are bisections
-// over the keys.  Only the others' mass is fp32; false where its error leaves
+// over the keys.  Only the others' mass is fp32 and in no units; false where its error leaves
 // top-p's cut open, or where a cut lies past the list.  For the whole block.
 constexpr int kPart = 256, kPer = kPart / 32;
 template <int NT>
@@ -684,7 +684,8 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
     } else {
       within = (double)block_reduce<NT>(sum, sm.red, Add{}, (int64_t)0);
       const double t = block_reduce<NT>(tail.v, sm.red, Add{}, 0.0) * unit;
-      const double err = Expo32::kErr * t;
+      // the fp32 weights' error, and what rounding every one of them to a unit may change
+      const double err = Expo32::kErr * t + (double)p.V;
       z_lo = within + t - err;
       z_hi = within + t + err;
     }

@@ -1,4 +1,5 @@
-"""Tree attention and sampling where the ranges of their number formats end."""
+"""Tree attention and sampling where the ranges of their number formats end: far weights in fp16, weights
+under the unit of sampling's integers."""
 import math
 
 import numpy as np
@@ -49,3 +50,50 @@ def test_far_weights_count(gpu, N, H, T, first, D, dt):
     rel = 2.0 ** -6.03 + 2.0 ** -10 if dt == "fp16" else 2.0 ** -7 + 2.0 ** -10
     err = np.abs(out.double().cpu().numpy() - want) / want
     assert err.max() <= rel, f"relative error {err.max():.3g}"
+
+
+# ------------------------------------------------------------------ sampling: weights under the unit
+
+def _sample(gpu, l, u, **kw):
+    M = len(l)
+    tok, lp = torch.full((M,), -7, dtype=torch.int32, device=DEV), torch.full((M,), math.nan, device=DEV)
+    dev = lambda a, t: torch.from_numpy(np.full(M, a, t)).to(DEV)  # noqa: E731
+    gpu.sample(l, torch.from_numpy(u).to(DEV), tok, lp,
+               **{k: dev(v, np.int32 if k == "top_k" else np.float32) for k, v in kw.items()})
+    return tok.cpu().numpy(), lp.cpu().numpy()
+
+
+def _check_units(gpu, l, u, **kw):
+    """l [M, V] and u [M] of rows that differ, or one row [V] and its u, M times over (kw: M)."""
+    M = kw.pop("M", len(l))
+    rows = l if l.ndim == 2 else l[None]
+    tok, lp = _sample(gpu, torch.from_numpy(rows).to(DEV).expand(M, -1).contiguous(),
+                      np.broadcast_to(np.asarray(u, np.float32), (M,)).copy(), **kw)
+    names = {"temperature": "T"}
+    V = rows.shape[1]
+    for m in range(len(rows)):
+        want = o64.sample_units(rows[m], float(np.float32(np.atleast_1d(u)[m])),
+                                **{names.get(k, k): v if k == "top_k" else float(np.float32(v)) for k, v in kw.items()})
+        # logprob: fp32 of a logarithm; the mass in it may come from fp32 weights (4.5e-7) and hold
+        # what the units drop (V half units)
+        tol = 2.0 ** -23 * abs(want[1]) + 4.5e-7 + V * 2.0 ** -(63 - (V - 1).bit_length())
+        same = slice(m, m + 1) if l.ndim == 2 else slice(None)
+        assert (tok[same] == want[0]).all(), (m, tok[same], want, kw)
+        assert (np.abs(lp[same] - want[1]) <= tol).all(), (m, lp[same], want, kw)
+
+
+@pytest.mark.parametrize("M", [3, 200])  # one row an SM, and several
+@pytest.mark.parametrize("V", [700, 32768])
+@pytest.mark.parametrize("T,tail", [(1.0, -40.0), (5.0, -200.0), (1.0, -60.0)])
+def test_top_p_ties_over_a_tail_of_nothing(gpu, M, V, T, tail):
+    """2 n equal tokens, the others' weights under half a unit: they count as 0, so exactly n tokens hold half of
+    the mass, whichever way the row takes."""
+    rng = np.random.default_rng(V + M)
+    for n in (1, 2, 40):
+        l = np.full((M, V), tail, np.float32)
+        for m in range(M):
+            l[m, rng.permutation(V)[:2 * n]] = 0.0
+        u = rng.random(M).astype(np.float32)
+        _check_units(gpu, l, u, temperature=T, top_p=0.5)
+        _check_units(gpu, l, u, temperature=T, top_p=0.5, top_k=V - 1)
+        _check_units(gpu, l, u, temperature=T, top_p=0.5, min_p=0.25)

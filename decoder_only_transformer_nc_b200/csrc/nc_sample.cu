@@ -13,9 +13,11 @@
 // definition here is in integers: a weight is computed in fp64 and rounded to
 // units of 2^-sh (sh = 62 less the bits of V, 51 at most: V weights of 1 do not
 // overflow), and sums are exact whatever their order.  A row is first tried
-// with fp32 weights, whose sums carry a bound of their error: where no border
-// (of top-p's share, of min-p, of the token's own interval) lies within it, the
-// integers would give the same token; only else are they computed.
+// with fp32 weights, whose sums carry a bound of their error and of what rounding
+// all V weights to units may change (V 2^-(sh + 1) of the mass: 1.2e-10 at V = 2^15,
+// 1.9e-9 at 2^17, 1.2e-7 at 2^20): where no border (of top-p's share, of min-p, of the
+// token's own interval) lies within it, the integers would give the same token; only
+// else are they computed.
 //
 // What bounds it: up to some hundred rows, latency (passes of a row that end at a
 // barrier, and code that is met for the first time: a row of 32768 logits, top-k 50
@@ -52,6 +54,7 @@ struct SampleParams {
   int32_t* tokens;           // [M]
   float* logprob;            // [M] or null
   int V, sh;
+  double slack;  // share of the mass by which sums of units and of true weights may differ
   int half;  // the histogram keeps a bin's mass as two sums of this many bits a token
 };
 
@@ -211,9 +214,9 @@ struct Expo32 {
     return fma(w, wide(e), w);
   }
   // What a - s z (a: a sum of some of the weights that z sums) may be off by: the
-  // errors of a count 1 - s times, those of the others s times.
-  __device__ static double off_by(double s, double a, double z, double err = kErr) {
-    return err * ((1.0 - s) * a + s * fmax(z - a, 0.0)) + 1e-9 * z;
+  // errors of a count 1 - s times, those of the others s times; and the units' rounding.
+  __device__ static double off_by(double s, double a, double z, double slack, double err = kErr) {
+    return err * ((1.0 - s) * a + s * fmax(z - a, 0.0)) + slack * z;
   }
 };
 
@@ -758,7 +761,7 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
 // errors leave its borders clear of the target.  The position in every lane of
 // the warp that finds it, -1 in the others.  For the whole block.
 template <int NT, bool EXACT, typename A, typename F>
-__device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& total, F kept,
+__device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& total, double slack, F kept,
                                       double err = Expo32::kErr) {
   constexpr int NW = NT / 32, U = EXACT ? 2 : 8;  // loads in flight
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -815,7 +818,8 @@ __device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& to
           const double up = (double)__shfl_sync(0xffffffffu, run + cum, h),
                        down = (double)__shfl_sync(0xffffffffu, run + cum - w, h);
           const double v = fmin(fmax((double)u, 0.0), 1.0);
-          if (!(up - target > Expo32::off_by(v, up, z, err)) || !(target - down > Expo32::off_by(v, down, z, err)))
+          if (!(up - target > Expo32::off_by(v, up, z, slack, err)) ||
+              !(target - down > Expo32::off_by(v, down, z, slack, err)))
             pick = -1;
         }
       }
@@ -897,7 +901,7 @@ __device__ __noinline__ int pick_plain(const Row r, float u, float T, double c, 
   if (__syncthreads_or(above)) return -1;
   double total;
   const int pick = locate<NT, false>(
-      r, sm, u, total, [&](int, float l) { return l > -INFINITY ? weight(l) : 0.0; },
+      r, sm, u, total, p.slack, [&](int, float l) { return l > -INFINITY ? weight(l) : 0.0; },
       FINE ? Expo32::kErrFine : Expo32::kErr);
   if (lane == 0 && pick >= 0) {
     p.tokens[row] = pick - r.off;
@@ -1080,7 +1084,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
               (q.n1 > 0 && (double)(za + cums[q.n1 - 1]) >= want));
       if (!EXACT && good) {  // and no token's border is within the error of what is wanted
         auto before = [&](int i) { return (double)(za + (i ? cums[i - 1] : A(0))); };
-        auto err = [&](double a) { return Expo32::off_by(pp, a, z); };
+        auto err = [&](double a) { return Expo32::off_by(pp, a, z, p.slack); };
         if (lo == 0)
           good = q.cnt_above == 0;
         else
@@ -1135,7 +1139,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     return w >= wmin ? w : A(0);
   };
   A total;
-  const int pick = locate<NT, EXACT>(r, sm, u, total, kept);
+  const int pick = locate<NT, EXACT>(r, sm, u, total, p.slack, kept);
   if (lane == 0 && pick >= 0) {
     const float l = r.base[pick];
     p.tokens[row] = pick - r.off;
@@ -1501,7 +1505,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
       collect<NT, 2>(r, list, sm.cand, NT, &sm.ncand,
                      [&](float l) { return l > -INFINITY && q.fbin(l) <= edge; });
       const double z = q.z * (double)((int64_t)1 << sh);
-      const int64_t z_lo = (int64_t)(z * (1.0 - Expo32::kErr)), z_hi = (int64_t)(z * (1.0 + Expo32::kErr)) + 1;
+      const double err = z * Expo32::kErr + (double)p.V;  // and the units' rounding
+      const int64_t z_lo = (int64_t)(z - err), z_hi = (int64_t)(z + err) + 1;
       if (pick_from_list<NT>(q.cnt_above + q.n1, INT_MAX, tp, z_lo, z_hi, wmin, u, weight, T, sm, p, row, r.off))
         return;
       __syncthreads();
@@ -1542,7 +1547,9 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   while (((int64_t)1 << bits) < V) ++bits;
   const int sh = 62 - bits < 51 ? 62 - bits : 51;
   const int half = 31 - bits < 15 ? 31 - bits : 15;  // V tokens in one bin do not overflow a sum
-  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, half};
+  // half a unit a token; 1e-9 more for the fp64 sums and the integers' own exponential
+  const double slack = 1e-9 + (double)V / (double)((int64_t)2 << sh);
+  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, slack, half};
   // Rows for every SM and more: some on each SM, they load and compute in turn (from
   // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
   if (M > device_sm_count()) return launch_t<256, false>(p, M, 8 * kPart * 8, stream);

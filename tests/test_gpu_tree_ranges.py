@@ -97,3 +97,18 @@ def test_top_p_ties_over_a_tail_of_nothing(gpu, M, V, T, tail):
         _check_units(gpu, l, u, temperature=T, top_p=0.5)
         _check_units(gpu, l, u, temperature=T, top_p=0.5, top_k=V - 1)
         _check_units(gpu, l, u, temperature=T, top_p=0.5, min_p=0.25)
+
+
+@pytest.mark.parametrize("M,V", [(1, 1 << 17), (1, 1 << 20), (1, 1 << 22), (150, 1 << 17), (150, 1 << 20)])
+def test_large_vocabularies_count_in_units(gpu, V, M):
+    """A tail of tokens just under half a unit (2^-sh, sh = 62 less the bits of V).  They count as 0 and are not
+    sampled, though together they are V / 2 units: 2^-24 of the mass at V = 2^20, 2^-20 at 2^22."""
+    sh = 62 - (V - 1).bit_length()
+    l = np.full(V, math.log(0.49) - sh * math.log(2.0), np.float32)
+    l[0] = 0.0
+    u = np.nextafter(np.float32(1), np.float32(0))
+    _check_units(gpu, l, u, M=M)
+    l[V // 3] = 0.0
+    for top_p in (0.5, 0.9):
+        _check_units(gpu, l, u, M=M, top_p=top_p)
+        _check_units(gpu, l, u, M=M, top_p=top_p, temperature=1.0, top_k=V // 2)

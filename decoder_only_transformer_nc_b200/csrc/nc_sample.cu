@@ -54,6 +54,7 @@ struct SampleParams {
   int32_t* tokens;           // [M]
   float* logprob;            // [M] or null
   int V, sh;
+  float unit2;   // 2^(1 - sh): two units
   double slack;  // share of the mass by which sums of units and of true weights may differ
   int half;  // the histogram keeps a bin's mass as two sums of this many bits a token
 };
@@ -951,7 +952,8 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   if (mp > 0.0f)
     wmin = EXACT ? (A)__double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << p.sh)) : (A)fminf(mp, 1.0f);
   const bool use_m = mp > 0.0f;
-  bool open = false;  // fp32: a weight too near min-p's border
+  bool open = false;  // fp32: a weight too near min-p's border: 1e-5 of it, or the two units by which
+  const float near = (float)wmin * 1e-5f + p.unit2;  // rounding the weight and the border may part them
   auto weight = [&](float l) -> A {
     if constexpr (EXACT) {
       return we(l);
@@ -1003,7 +1005,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
       walk4<1>(r, [&](int, const float4& v) {
         float w0 = wf(v.x), w1 = wf(v.y), w2 = wf(v.z), w3 = wf(v.w);
         if (use_m) {
-          const float m = (float)wmin, near = m * 1e-5f;
+          const float m = (float)wmin;
           open = open || fabsf(w0 - m) <= near || fabsf(w1 - m) <= near || fabsf(w2 - m) <= near ||
                  fabsf(w3 - m) <= near;
           w0 = w0 >= m ? w0 : 0.0f;
@@ -1035,7 +1037,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
           const float m = (float)wmin;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            open = open || fabsf(a[e] - m) <= m * 1e-5f;
+            open = open || fabsf(a[e] - m) <= near;
             a[e] = a[e] >= m ? a[e] : 0.0f;
           }
           ms.add(a[0], a[1], a[2], a[3]);
@@ -1103,7 +1105,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
         const int at = (int)~(uint32_t)sm.cand[i];
         const A w = weight(value_of((uint32_t)(sm.cand[i] >> 32)));
         if (at >= r.seg0 && at < r.seg1 && w >= wmin) add += w;
-        if (!EXACT && use_m) open = open || fabs((double)w - (double)wmin) <= (double)wmin * 1e-5;
+        if (!EXACT && use_m) open = open || fabs((double)w - (double)wmin) <= (double)near;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
@@ -1322,7 +1324,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     // of every segment (in 64 steps of T / 4).  Where those tokens' likely ones hold
     // far less than top-p's share, the list would be made in vain (10 of 60 us at
     // 32768 tokens).
-    float least = mx + logf(fminf(mp, 1.0f)) * T * 1.00001f - 1e-5f * T - fabsf(mx) * 1e-6f;
+    // (a weight that rounds to min-p's units may be under it: two units less)
+    float least = mx + logf(fmaxf(fminf(mp, 1.0f) - p.unit2, 0.0f)) * T * 1.00001f - 1e-5f * T - fabsf(mx) * 1e-6f;
     bool enough = true;
     if (use_p || k > 0) {
       const Expo32 wf(mx, sm.c, T);
@@ -1549,7 +1552,8 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   const int half = 31 - bits < 15 ? 31 - bits : 15;  // V tokens in one bin do not overflow a sum
   // half a unit a token; 1e-9 more for the fp64 sums and the integers' own exponential
   const double slack = 1e-9 + (double)V / (double)((int64_t)2 << sh);
-  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, slack, half};
+  const float unit2 = (float)(1.0 / (double)((int64_t)1 << (sh - 1)));
+  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, unit2, slack, half};
   // Rows for every SM and more: some on each SM, they load and compute in turn (from
   // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
   if (M > device_sm_count()) return launch_t<256, false>(p, M, 8 * kPart * 8, stream);

@@ -112,3 +112,17 @@ def test_large_vocabularies_count_in_units(gpu, V, M):
     for top_p in (0.5, 0.9):
         _check_units(gpu, l, u, M=M, top_p=top_p)
         _check_units(gpu, l, u, M=M, top_p=top_p, temperature=1.0, top_k=V // 2)
+
+
+@pytest.mark.parametrize("M", [2, 160])
+@pytest.mark.parametrize("units,kept", [(127.6, True), (127.4, False)])
+@pytest.mark.parametrize("kw", [{}, dict(top_p=0.9999999), dict(top_k=30000)], ids=["m", "mp", "mk"])
+def test_min_p_of_a_few_units(gpu, M, units, kept, kw):
+    """min_p = 2^-40 is 128 units at V = 32768; weights of 127.6 are 128 of them and kept, of 127.4 are not.  With u = 2^-26
+    the kept ones, 2^-25 of the mass before the largest token, hold the target."""
+    V, sh = 32768, 47
+    l = np.full(V, math.log(units) - sh * math.log(2.0), np.float32)
+    l[-1] = 0.0
+    _check_units(gpu, l, 2.0 ** -26, M=M, min_p=2.0 ** -40, **kw)
+    want = o64.sample_units(l, 2.0 ** -26, min_p=2.0 ** -40)[0]
+    assert (want < V - 1) == kept  # the case is what it says

@@ -22,6 +22,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -1093,6 +1094,42 @@ nc_status nc_decode_step_dev(const nc_config* cfg, const nc_weights* w, const in
 }  // extern "C"
 
 // ---------------------------------------------------------------- drafted trees, sampling, distillation
+namespace {
+
+// An array of a call: where it starts and how many bytes it has (NULL: none).
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
+}
+
+// Whether an output overlaps an input or another output.
+bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* q = outs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return true;
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return true;
+  }
+  return false;
+}
+
+// The arrays of an acceptance: the CTAs of every layer walk the tree again from the
+// inputs while those of layer 0 write the path.
+bool accept_overlap(const int32_t* tokens, const int32_t* parents, const uint32_t* mask, const int32_t* sampled,
+                    const int32_t* lens, const int32_t* path, const int32_t* count, const int32_t* next,
+                    const int32_t* lens_out, int B, int N, Span kv, Span cache) {
+  const int64_t rows = (int64_t)B * 4, nodes = rows * N;
+  return any_overlap({{path, nodes}, {count, rows}, {next, rows}, {lens_out, rows}, cache},
+                     {{tokens, nodes}, {parents, nodes}, {mask, nodes * ((N + 31) / 32)}, {sampled, nodes}, {lens, rows}, kv});
+}
+
+}  // namespace
+
 extern "C" {
 
 nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, void* stream) {
@@ -1139,6 +1176,10 @@ nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const ui
       (int64_t)Hkv * D % 4 != 0)
     return NC_ERR_SHAPE;
   if (!aligned16(kv) || !aligned16(cache)) return NC_ERR_ALIGNMENT;
+  const int64_t row = (int64_t)L * B * 2 * Hkv * D * 2;  // bytes of one position or node of every layer and row
+  if (accept_overlap(tokens, parents, mask, sampled, lens, path, count, next, lens_out, B, N, {kv, row * N},
+                     {cache, row * T_max}))
+    return NC_ERR_INVALID_ARG;
   if (nc_status s = device_ok()) return s;
   return tree_accept_launch(tokens, parents, mask, sampled, lens, kv, cache, path, count, next, lens_out, nullptr, B,
                             N, L, T_max, 2 * Hkv * D, S(stream));
@@ -1345,9 +1386,12 @@ nc_status nc_accept_tree(const nc_config* cfg, const int32_t* tokens, const int3
       !session || !workspace)
     return NC_ERR_INVALID_ARG;
   if (nc_status s = tree_step_check(cfg, B, N, session, session_bytes, T_max, workspace, ws_bytes)) return s;
-  if (nc_status s = device_ok()) return s;
   const SessionLayout SL = session_layout(cfg, B, T_max);
   const TreeLayout TL = tree_layout(cfg, B, N);
+  if (accept_overlap(tokens, parents, nullptr, sampled, lens, path, count, next, lens_out, B, N,
+                     {workspace, (int64_t)TL.total}, {session, (int64_t)SL.total}))
+    return NC_ERR_INVALID_ARG;
+  if (nc_status s = device_ok()) return s;
   uint8_t* base = static_cast<uint8_t*>(session);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int32_t* hist = (cfg->extras & NC_EXTRA_SMEAR) ? reinterpret_cast<int32_t*>(base + SL.hist) : nullptr;

@@ -312,7 +312,8 @@ nc_status nc_decode_tree(const nc_config* cfg, const nc_weights* w, const int32_
 
 /* nc_tree_accept over every layer of the session, after nc_decode_tree of the
  * same tokens, parents, lens and workspace; with NC_EXTRA_SMEAR the accepted
- * tokens are recorded too.  sampled [B, N]: the token sampled at each node. */
+ * tokens are recorded too.  sampled [B, N]: the token sampled at each node.  path,
+ * count, next and lens_out may overlap neither the inputs nor one another. */
 nc_status nc_accept_tree(const nc_config* cfg, const int32_t* tokens, const int32_t* parents, const int32_t* sampled,
                          const int32_t* lens, int B, int N, int32_t* path, int32_t* count, int32_t* next,
                          int32_t* lens_out, void* session, size_t session_bytes, int T_max, void* workspace,
@@ -655,7 +656,8 @@ nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint1
  *   lens_out [B] = lens (clamped to [0, T_max]) + count;
  *   cache[l, b, lens[b] + k] = kv[l, b, path[b][k]] for every layer l < L.
  * kv [L, B, N, 2, Hkv, D], cache [L, B, T_max, 2, Hkv, D] 16-bit; mask as
- * nc_tree_mask writes it.  lens_out may not be lens.  1 <= N <= 128,
+ * nc_tree_mask writes it.  No output (the cache among them) may overlap an input
+ * or another output.  1 <= N <= 128,
  * 1 <= L <= 65535, Hkv D a multiple of 4.  One launch. */
 nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const uint32_t* mask, const int32_t* sampled,
                          const int32_t* lens, const uint16_t* kv, uint16_t* cache, int32_t* path, int32_t* count,

@@ -1,0 +1,57 @@
+"""Calls whose outputs overlap their inputs or one another are refused before anything runs (CPU only: addresses
+that nothing dereferences)."""
+import ctypes
+import itertools
+
+P = 1 << 40  # each array has its own 2^30 bytes from here on
+
+
+def _places(names):
+    return {n: P + (i << 30) for i, n in enumerate(names)}
+
+
+def test_tree_accept_overlaps(nclib):
+    L = nclib.lib()
+    B, N, layers, Hkv, D, T = 2, 40, 3, 2, 64, 128
+    names = ["tokens", "parents", "mask", "sampled", "lens", "kv", "cache", "path", "count", "next", "lens_out"]
+    size = dict(tokens=B * N * 4, parents=B * N * 4, mask=B * N * 8, sampled=B * N * 4, lens=B * 4, count=B * 4, next=B * 4,
+                lens_out=B * 4, path=B * N * 4, kv=layers * B * N * 2 * Hkv * D * 2, cache=layers * B * T * 2 * Hkv * D * 2)
+
+    def code(**at):
+        return L.nc_tree_accept(*{**_places(names), **at}.values(), B, N, layers, Hkv, D, T, None)
+
+    assert code() == 8  # nothing but the device is wrong
+    outs = ["cache", "path", "count", "next", "lens_out"]
+    for o, i in itertools.permutations(names, 2):
+        if o not in outs and i not in outs:
+            continue
+        base = _places(names)[i]
+        # the same start, the last 16 bytes (4 of the small ones), and just beside
+        assert code(**{o: base}) == 1, (o, i)
+        step = 16 if size[i] >= 16 and size[i] % 16 == 0 else 4
+        if o not in ("kv", "cache") or step == 16:
+            assert code(**{o: base + size[i] - step}) == 1, (o, i)
+            assert code(**{o: base + size[i] + 16 - size[i] % 16}) == 8, (o, i)
+    # inputs may share memory
+    assert code(tokens=_places(names)["sampled"], parents=_places(names)["sampled"]) == 8
+
+
+def test_accept_tree_overlaps(nclib):
+    L = nclib.lib()
+    c = nclib.init_config(2, 64, 64, 0, 256, 512)
+    B, N, T = 2, 8, 64
+    sb, wb = L.nc_session_bytes(ctypes.byref(c), B, T), nclib.tree_workspace_bytes(c, B, N)
+    names = ["tokens", "parents", "sampled", "lens", "path", "count", "next", "lens_out", "session", "ws"]
+
+    def code(**at):
+        a = {**_places(names), **at}
+        return L.nc_accept_tree(ctypes.byref(c), *[a[k] for k in names[:4]], B, N, *[a[k] for k in names[4:8]], a["session"],
+                                sb, T, a["ws"], wb, None)
+
+    assert code() == 8
+    for o in names[4:8]:
+        for i in names:
+            if i != o:
+                assert code(**{o: _places(names)[i]}) == 1, (o, i)
+                assert code(**{o: _places(names)[i] + 4}) == 1, (o, i)
+    assert code(path=P + (9 << 30) + wb - 4) == 1 and code(path=P + (9 << 30) + wb) == 8

@@ -1205,6 +1205,11 @@ nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const floa
       (dz == nullptr) != (dz_dtype == NC_GRAD_NONE) || dz == z)
     return NC_ERR_INVALID_ARG;
   if (V < 1 || V > (1 << 24) || K < 1 || K > 1024) return NC_ERR_SHAPE;
+  // the CTAs of a row read its weight and the teacher's entries after its loss may be stored
+  const int64_t m = M, dz_size = dz_dtype == NC_GRAD_F32 ? 4 : 2;
+  if (any_overlap({{dz, m * V * dz_size}, {token_loss, m * 4}},
+                  {{z, m * V * 4}, {teacher_idx, m * K * 4}, {teacher_logits, m * K * 4}, {row_weight, m * 4}}))
+    return NC_ERR_INVALID_ARG;
   if (nc_status s = device_ok()) return s;
   const int kind = dz_dtype == NC_GRAD_NONE ? 0 : dz_dtype == NC_GRAD_F32 ? 1 : dz_dtype == NC_GRAD_BF16 ? 2 : 3;
   return distill_topk_launch(z, teacher_idx, teacher_logits, row_weight, token_loss, dz, kind, M, V, K, tau, cap,

@@ -705,8 +705,8 @@ typedef enum { NC_GRAD_BF16 = 0, NC_GRAD_F16 = 1, NC_GRAD_F32 = 2, NC_GRAD_NONE 
  * NC_DEV_TARGET_RANGE; an index may occur more than once.  A row with no entry
  * has loss 0 and gradient 0.  fp16 gradients saturate at +-65504.  2^-16 <= tau
  * <= 2^16, cap 0 or in the same range, 1 <= K <= 1024, 1 <= V <= 2^24.  z needs a
- * finite maximum in each row, teacher logits are finite or -inf.  dz may not
- * overlap z.  dev_status (or NULL) also gets NC_DEV_TIMEOUT if the parts of a row
+ * finite maximum in each row, teacher logits are finite or -inf.  dz and
+ * token_loss may overlap neither the inputs nor each other.  dev_status (or NULL) also gets NC_DEV_TIMEOUT if the parts of a row
  * did not meet in time (its outputs are not written then).  Same result run to
  * run. */
 nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const float* teacher_logits,

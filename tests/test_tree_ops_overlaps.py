@@ -55,3 +55,30 @@ def test_accept_tree_overlaps(nclib):
                 assert code(**{o: _places(names)[i]}) == 1, (o, i)
                 assert code(**{o: _places(names)[i] + 4}) == 1, (o, i)
     assert code(path=P + (9 << 30) + wb - 4) == 1 and code(path=P + (9 << 30) + wb) == 8
+
+
+def test_distill_overlaps(nclib):
+    L = nclib.lib()
+    M, V, K = 6, 70, 8
+    names = ["z", "idx", "teacher", "weight", "loss", "dz"]
+    size = dict(z=M * V * 4, idx=M * K * 4, teacher=M * K * 4, weight=M * 4, loss=M * 4)
+    for dt, es in ((0, 2), (1, 2), (2, 4), (3, 0)):
+        size["dz"] = M * V * es
+
+        def code(**at):
+            a = {**_places(names), **at}
+            if not es:
+                a["dz"] = None
+            return L.nc_distill_topk(*[a[k] for k in names], dt, M, V, K, 1.0, 15.0, None, None)
+
+        assert code() == 8 and code(weight=None) == 8
+        for o in ["loss", "dz"] if es else ["loss"]:
+            for i in names:
+                if i == o or not size[i]:
+                    continue
+                base = _places(names)[i]
+                assert code(**{o: base}) == 1, (o, i)
+                assert code(**{o: base + size[i] - 4}) == 1, (o, i)
+                assert code(**{o: base - size[o] + 4}) == 1, (o, i)
+                assert code(**{o: base + size[i]}) == 8 and code(**{o: base - size[o]}) == 8, (o, i)
+        assert code(weight=_places(names)["teacher"]) == 8  # inputs may share memory

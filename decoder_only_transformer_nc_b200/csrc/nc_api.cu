@@ -1135,6 +1135,8 @@ extern "C" {
 nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, void* stream) {
   if (!parents || !mask || B < 0) return NC_ERR_INVALID_ARG;
   if (N < 1 || N > kTreeMaxNodes) return NC_ERR_SHAPE;
+  const int64_t nodes = (int64_t)B * N * 4;
+  if (any_overlap({{mask, nodes * ((N + 31) / 32)}}, {{parents, nodes}})) return NC_ERR_INVALID_ARG;
   if (nc_status s = device_ok()) return s;
   return tree_mask_launch(parents, mask, B, N, S(stream));
 }
@@ -1160,6 +1162,14 @@ nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint1
     return NC_ERR_ALIGNMENT;
   const size_t need = tree_attention_bytes(B, N, H, Hkv, D, T_max, window);
   if (need > 0 && (!workspace || ws_bytes < need)) return NC_ERR_WORKSPACE;
+  // out may be q itself: a row of q is read by the CTAs of its kv head alone, before its output is written
+  const int64_t BN = (int64_t)B * N, row = (int64_t)2 * Hkv * D * 2;
+  const Span o{out, BN * H * D * 2}, query{q, B > 0 ? ((BN - 1) * q_row_stride + (int64_t)H * D) * 2 : 0};
+  if (any_overlap({o, {need > 0 ? workspace : nullptr, (int64_t)need}},
+                  {{kv, BN * row}, {cache, (int64_t)B * T_max * row}, {lens, (int64_t)B * 4}, {mask, BN * ((N + 31) / 32) * 4}}) ||
+      (overlap(o, query) && (out != q || q_row_stride != (int64_t)H * D)) ||
+      (need > 0 && overlap(query, {workspace, (int64_t)need})))
+    return NC_ERR_INVALID_ARG;
   if (nc_status s = device_ok()) return s;
   return tree_attention_launch(q, q_row_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window,
                                dtype == NC_F16, workspace, dev_status, S(stream));
@@ -1191,6 +1201,13 @@ nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, con
   if (!logits || !u || !tokens || M < 0) return NC_ERR_INVALID_ARG;
   if (V < 1 || V > (1 << 24)) return NC_ERR_SHAPE;
   if (row_stride < V) return NC_ERR_INVALID_ARG;
+  // a row reads its numbers before it writes its own: the same array will do, one shifted by rows will not
+  const int64_t rows = (int64_t)M * 4;
+  const Span tok{tokens, rows}, lp{logprob, rows};
+  if (any_overlap({tok, lp}, {{logits, M > 0 ? (((int64_t)M - 1) * row_stride + V) * 4 : 0}})) return NC_ERR_INVALID_ARG;
+  for (const void* in : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p})
+    for (const Span& out : {tok, lp})
+      if (overlap(out, {in, rows}) && out.at != in) return NC_ERR_INVALID_ARG;
   if (nc_status s = device_ok()) return s;
   return sample_launch(logits, row_stride, u, temperature, top_k, top_p, min_p, tokens, logprob, M, V, S(stream));
 }

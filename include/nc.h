@@ -621,7 +621,8 @@ nc_status nc_lm_head_loss_static(const uint16_t* a, const uint16_t* w_lm, const 
 
 /* mask [B, N, ceil(N / 32)] from parents [B, N] (1 <= N <= 128): bit j % 32 of
  * word j / 32 of node i is set where j is i or an ancestor of i.  A node whose
- * walk up leaves [0, i) before it ends at a root (-1) is unused: all bits 0. */
+ * walk up leaves [0, i) before it ends at a root (-1) is unused: all bits 0.
+ * mask may not overlap parents. */
 nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, void* stream);
 
 /* Attention of the N drafted nodes of every row over the cache and their own
@@ -638,7 +639,8 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * at and past N are 0.  K and V of committed positions inside the root's window
  * and of used nodes must be finite.  workspace: at least
  * nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where that is
- * 0); calls that overlap in time need one each.  dev_status (or NULL) gets
+ * 0); calls that overlap in time need one each.  out may be q (of q_row_stride
+ * H D); else neither it nor the workspace may overlap an input.  dev_status (or NULL) gets
  * NC_DEV_TIMEOUT if a pipeline wait ran out (out is not valid then).  The result
  * is the same run to run. */
 size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window);
@@ -682,7 +684,8 @@ nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const ui
  * V <= 32768; smaller ones count as 0) and exact sums, the same run to run.
  * logprob may come from fp32 weights: the mass in it is within 4.5e-7 of each
  * weight, relative (a few 1e-8 in practice).  A row whose copy to the SM does not
- * arrive in time gives token -1 and logprob NaN.
+ * arrive in time gives token -1 and logprob NaN.  tokens and logprob may overlap
+ * neither the logits nor each other, and of the arrays per row only one as a whole.
  * 1 <= V <= 2^24. */
 nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, const float* temperature,
                     const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, float* logprob,

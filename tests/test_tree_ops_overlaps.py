@@ -82,3 +82,60 @@ def test_distill_overlaps(nclib):
                 assert code(**{o: base - size[o] + 4}) == 1, (o, i)
                 assert code(**{o: base + size[i]}) == 8 and code(**{o: base - size[o]}) == 8, (o, i)
         assert code(weight=_places(names)["teacher"]) == 8  # inputs may share memory
+
+
+def test_tree_mask_overlaps(nclib):
+    L = nclib.lib()
+    for N, W in ((20, 1), (40, 2)):
+        assert L.nc_tree_mask(P, P + 3 * N * 4, 3, N, None) == 8 and L.nc_tree_mask(P + 3 * N * W * 4, P, 3, N, None) == 8
+        for d in (0, 4, 3 * N * 4 - 4):
+            assert L.nc_tree_mask(P, P + d, 3, N, None) == 1
+        assert L.nc_tree_mask(P + 3 * N * W * 4 - 4, P, 3, N, None) == 1
+
+
+def test_tree_attention_overlaps(nclib):
+    L = nclib.lib()
+    names = ["q", "kv", "cache", "lens", "mask", "out", "ws"]
+    for B, N, H, Hkv, D, T, stride in ((2, 4, 4, 2, 64, 96, 256), (2, 64, 4, 2, 128, 900, 512), (1, 3, 4, 4, 64, 96, 768)):
+        W = (N + 31) // 32
+        need = L.nc_tree_attention_workspace_bytes(B, N, H, Hkv, D, T, 0)
+        size = dict(q=((B * N - 1) * stride + H * D) * 2, kv=B * N * 2 * Hkv * D * 2, cache=B * T * 2 * Hkv * D * 2, lens=B * 4,
+                    mask=B * N * W * 4, out=B * N * H * D * 2, ws=need)
+
+        def code(**at):
+            a = {**_places(names), **at}
+            return L.nc_tree_attention(a["q"], stride, a["kv"], a["cache"], a["lens"], a["mask"], a["out"], B, N, H, Hkv, D, T, 0,
+                                       1, a["ws"] if need else None, need, None, None)
+
+        assert code() == 8
+        for o in ("out", "ws") if need else ("out",):
+            for i in names:
+                if i == o or not size[i]:
+                    continue
+                base = _places(names)[i]
+                whole = o == "out" and i == "q" and stride == H * D
+                assert code(**{o: base}) == (8 if whole else 1), (o, i)
+                assert code(**{o: base + (size[i] - 1) // 16 * 16}) == 1, (o, i)
+                assert code(**{o: base + (size[i] + 15) // 16 * 16}) == 8, (o, i)
+
+
+def test_sample_overlaps(nclib):
+    L = nclib.lib()
+    M, V, ld = 6, 70, 100
+    names = ["logits", "u", "t", "k", "p", "m", "tokens", "logprob"]
+
+    def code(**at):
+        a = {**_places(names), **at}
+        return L.nc_sample(a["logits"], ld, a["u"], a["t"], a["k"], a["p"], a["m"], a["tokens"], a["logprob"], M, V, None)
+
+    assert code() == 8 and code(logprob=None) == 8
+    end = ((M - 1) * ld + V) * 4
+    for o in ("tokens", "logprob"):
+        assert code(**{o: _places(names)["logits"]}) == 1 and code(**{o: _places(names)["logits"] + end - 4}) == 1
+        assert code(**{o: _places(names)["logits"] + end}) == 8
+        for i in names[1:]:
+            if i == o:
+                continue
+            base = _places(names)[i]
+            assert code(**{o: base}) == (1 if i in ("tokens", "logprob") else 8), (o, i)
+            assert code(**{o: base + 4}) == 1 and code(**{o: base - 4}) == 1 and code(**{o: base + M * 4}) == 8, (o, i)

@@ -417,13 +417,17 @@ __device__ __forceinline__ void distill_part(const DistillParams& p, int slice, 
   }
   if (warp != 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   {
+    // A part that comes too late to count is still waited for, as long again: it lands in
+    // this CTA's shared memory, which must be there.
     bool late = false;
     if (!mbar_try_wait_cluster(smem_u32(&sh.bar), 0)) {
       const uint64_t t0 = global_timer_ns();
-      for (uint32_t it = 1; !late && !mbar_try_wait_cluster(smem_u32(&sh.bar), 0); ++it)
-        if ((it & 255u) == 0u) late = global_timer_ns() - t0 > kWaitLimitNs;
+      uint64_t waited = 0;
+      for (uint32_t it = 1; waited <= 2 * kWaitLimitNs && !mbar_try_wait_cluster(smem_u32(&sh.bar), 0); ++it)
+        if ((it & 255u) == 0u) waited = global_timer_ns() - t0;
+      late = waited > kWaitLimitNs;
     }
-    if (__any_sync(0xffffffffu, late)) {  // a CTA of the cluster never came: nothing is written
+    if (__any_sync(0xffffffffu, late)) {  // this warp writes nothing (others may have seen the parts in time)
       if (lane == 0 && p.status) atomicOr(p.status, NC_DEV_TIMEOUT);
       if (DZ != 0 && !helper) named_arrive(2, kBlock);
       return;

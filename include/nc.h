@@ -709,9 +709,10 @@ typedef enum { NC_GRAD_BF16 = 0, NC_GRAD_F16 = 1, NC_GRAD_F32 = 2, NC_GRAD_NONE 
  * has loss 0 and gradient 0.  fp16 gradients saturate at +-65504.  2^-16 <= tau
  * <= 2^16, cap 0 or in the same range, 1 <= K <= 1024, 1 <= V <= 2^24.  z needs a
  * finite maximum in each row, teacher logits are finite or -inf.  dz and
- * token_loss may overlap neither the inputs nor each other.  dev_status (or NULL) also gets NC_DEV_TIMEOUT if the parts of a row
- * did not meet in time (its outputs are not written then).  Same result run to
- * run. */
+ * token_loss may overlap neither the inputs nor each other.  dev_status (or
+ * NULL) also gets NC_DEV_TIMEOUT if the parts of a row did not meet in time: its
+ * loss and gradient are not valid then (not written, or in part).  Same result
+ * run to run. */
 nc_status nc_distill_topk(const float* z, const int32_t* teacher_idx, const float* teacher_logits,
                           const float* row_weight, float* token_loss, void* dz, nc_grad_dtype dz_dtype, int M, int V,
                           int K, float tau, float cap, uint32_t* dev_status, void* stream);

@@ -1198,9 +1198,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     if (b < r.seg1 && lane < r.seg1 - b && b + lane >= r.off) staged[b + lane] = r.base[b + lane];
     __syncwarp();
     r.base = staged;
-    if (a < b) {
+    if (a < b) {  // a copy that comes too late is still waited for, as long again: its target must be there
       const uint64_t t0 = global_timer_ns();
-      while (!late && !mbar_try_wait(smem_u32(&sm.bar[warp]), 0)) late = global_timer_ns() - t0 > kWaitLimitNs;
+      uint64_t waited = 0;
+      while (waited <= 2 * kWaitLimitNs && !mbar_try_wait(smem_u32(&sm.bar[warp]), 0)) waited = global_timer_ns() - t0;
+      late = waited > kWaitLimitNs;
     }
   }
   if (T > 0.0f && u < 1.0f && tp >= 1.0f && !(mp > 0.0f) && (k <= 0 || k >= p.V)) {

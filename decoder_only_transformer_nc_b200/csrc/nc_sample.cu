@@ -54,10 +54,17 @@ struct SampleParams {
   int32_t* tokens;           // [M]
   float* logprob;            // [M] or null
   int V, sh;
-  float unit2;   // 2^(1 - sh): two units
-  double slack;  // share of the mass by which sums of units and of true weights may differ
   int half;  // the histogram keeps a bin's mass as two sums of this many bits a token
 };
+
+// The share of the mass by which sums of units and of true weights may differ: half a
+// unit a token, and 1e-9 for the fp64 sums and the integers' own exponential.
+__device__ __forceinline__ double slack_of(const SampleParams& p) {
+  return fma((double)p.V, __hiloint2double((1022 - p.sh) << 20, 0), 1e-9);
+}
+
+// Two units: by so much rounding a weight and min-p to units may part them.
+__device__ __forceinline__ float two_units(const SampleParams& p) { return __int_as_float((128 - p.sh) << 23); }
 
 // Order-preserving map of a logit to 32 bits; -0 equals +0, NaN is below
 // everything (key 0).
@@ -345,7 +352,7 @@ constexpr int kTopBins = 256;  // histogram of the threads' maxima
 
 template <int NT>
 struct Smem {
-  double tab[32], c;  // log2(e) / T
+  double tab[32], c, slack;  // c: log2(e) / T
   int64_t red[32];
   float redf[2][32];
   int64_t seg[32];
@@ -762,7 +769,7 @@ __device__ __noinline__ bool pick_from_top(const Row r, int k, float tp, float m
 // errors leave its borders clear of the target.  The position in every lane of
 // the warp that finds it, -1 in the others.  For the whole block.
 template <int NT, bool EXACT, typename A, typename F>
-__device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& total, double slack, F kept,
+__device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& total, F kept,
                                       double err = Expo32::kErr) {
   constexpr int NW = NT / 32, U = EXACT ? 2 : 8;  // loads in flight
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -819,6 +826,7 @@ __device__ __forceinline__ int locate(const Row& r, Smem<NT>& sm, float u, A& to
           const double up = (double)__shfl_sync(0xffffffffu, run + cum, h),
                        down = (double)__shfl_sync(0xffffffffu, run + cum - w, h);
           const double v = fmin(fmax((double)u, 0.0), 1.0);
+          const double slack = sm.slack;
           if (!(up - target > Expo32::off_by(v, up, z, slack, err)) ||
               !(target - down > Expo32::off_by(v, down, z, slack, err)))
             pick = -1;
@@ -902,7 +910,7 @@ __device__ __noinline__ int pick_plain(const Row r, float u, float T, double c, 
   if (__syncthreads_or(above)) return -1;
   double total;
   const int pick = locate<NT, false>(
-      r, sm, u, total, p.slack, [&](int, float l) { return l > -INFINITY ? weight(l) : 0.0; },
+      r, sm, u, total, [&](int, float l) { return l > -INFINITY ? weight(l) : 0.0; },
       FINE ? Expo32::kErrFine : Expo32::kErr);
   if (lane == 0 && pick >= 0) {
     p.tokens[row] = pick - r.off;
@@ -952,8 +960,8 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
   if (mp > 0.0f)
     wmin = EXACT ? (A)__double2ll_ru((double)fminf(mp, 1.0f) * (double)((int64_t)1 << p.sh)) : (A)fminf(mp, 1.0f);
   const bool use_m = mp > 0.0f;
-  bool open = false;  // fp32: a weight too near min-p's border: 1e-5 of it, or the two units by which
-  const float near = (float)wmin * 1e-5f + p.unit2;  // rounding the weight and the border may part them
+  bool open = false;  // fp32: a weight too near min-p's border
+  const float near = (float)wmin * 1e-5f + two_units(p);
   auto weight = [&](float l) -> A {
     if constexpr (EXACT) {
       return we(l);
@@ -1086,7 +1094,8 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
               (q.n1 > 0 && (double)(za + cums[q.n1 - 1]) >= want));
       if (!EXACT && good) {  // and no token's border is within the error of what is wanted
         auto before = [&](int i) { return (double)(za + (i ? cums[i - 1] : A(0))); };
-        auto err = [&](double a) { return Expo32::off_by(pp, a, z, p.slack); };
+        const double slack = sm.slack;
+        auto err = [&](double a) { return Expo32::off_by(pp, a, z, slack); };
         if (lo == 0)
           good = q.cnt_above == 0;
         else
@@ -1141,7 +1150,7 @@ __device__ __noinline__ bool pick_from_row(const Row r, const Cut q, float tp, f
     return w >= wmin ? w : A(0);
   };
   A total;
-  const int pick = locate<NT, EXACT>(r, sm, u, total, p.slack, kept);
+  const int pick = locate<NT, EXACT>(r, sm, u, total, kept);
   if (lane == 0 && pick >= 0) {
     const float l = r.base[pick];
     p.tokens[row] = pick - r.off;
@@ -1172,7 +1181,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
   const int sh = p.sh;
   const float T = p.temperature ? p.temperature[row] : 1.0f;
   if (tid < 32) sm.tab[tid] = kExp2[tid];
-  if (tid == 32) sm.c = 1.4426950408889634 / (double)T;
+  if (tid == 32) {
+    sm.c = 1.4426950408889634 / (double)T;
+    sm.slack = slack_of(p);
+  }
   const float u = p.u[row];
   int k = p.top_k ? p.top_k[row] : 0;
   const float tp = p.top_p ? p.top_p[row] : 1.0f;
@@ -1327,7 +1339,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) sample_kernel(const Sam
     // far less than top-p's share, the list would be made in vain (10 of 60 us at
     // 32768 tokens).
     // (a weight that rounds to min-p's units may be under it: two units less)
-    float least = mx + logf(fmaxf(fminf(mp, 1.0f) - p.unit2, 0.0f)) * T * 1.00001f - 1e-5f * T - fabsf(mx) * 1e-6f;
+    float least = mx + logf(fmaxf(fminf(mp, 1.0f) - two_units(p), 0.0f)) * T * 1.00001f - 1e-5f * T - fabsf(mx) * 1e-6f;
     bool enough = true;
     if (use_p || k > 0) {
       const Expo32 wf(mx, sm.c, T);
@@ -1552,10 +1564,7 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   while (((int64_t)1 << bits) < V) ++bits;
   const int sh = 62 - bits < 51 ? 62 - bits : 51;
   const int half = 31 - bits < 15 ? 31 - bits : 15;  // V tokens in one bin do not overflow a sum
-  // half a unit a token; 1e-9 more for the fp64 sums and the integers' own exponential
-  const double slack = 1e-9 + (double)V / (double)((int64_t)2 << sh);
-  const float unit2 = (float)(1.0 / (double)((int64_t)1 << (sh - 1)));
-  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, unit2, slack, half};
+  const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, half};
   // Rows for every SM and more: some on each SM, they load and compute in turn (from
   // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
   if (M > device_sm_count()) return launch_t<256, false>(p, M, 8 * kPart * 8, stream);

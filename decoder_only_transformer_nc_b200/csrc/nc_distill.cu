@@ -8,7 +8,9 @@
 //
 // An entry with index -1 is unused (rows with fewer teacher entries than K); an
 // index outside [-1, V) is flagged and unused.  A row with no entry has loss 0
-// and gradient 0.  Softmax statistics and sums are fp32 in a fixed order.
+// and gradient 0.  Softmax statistics and sums are fp32 in a fixed order; exponentials and
+// reciprocals are the hardware's (2^-22 relative) and the scale cap log2(e) / tau is rounded
+// once, which leaves the loss within some 5e-7 of the 64-bit one (fp32 with exp: 1e-7).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -183,7 +185,9 @@ __device__ __forceinline__ float2 join8(float2 v) {
 // logits, eight warps repeating it took as many instructions as the row.  That warp
 // takes longer than the row from K = 128 or so (4096 rows without a gradient: 117 us
 // at K = 64, 330 at 512).
-// REGS = 0: longer rows, one CTA, read again from L2 for each use.
+// REGS = 0: rows of more than 65536 logits, one CTA each, read again from L2 for each
+// use.  1024 rows of 131072, K = 64: 377 us with a bf16 gradient (floor 123 at the copy
+// rate), 173 without (82); 8 rows of them take 151 us, of 65536 logits 7 us.
 // Groups of four start at 16-byte boundaries of z's row; the row's ends and a dz that
 // is not aligned alike go by single elements.  2048 rows of 32767 logits without a
 // gradient take 86 us (106 while every group was tested for the ends), those of 32768

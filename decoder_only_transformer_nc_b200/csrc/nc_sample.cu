@@ -1567,6 +1567,10 @@ nc_status sample_launch(const float* logits, int64_t ld, const float* u, const f
   const SampleParams p{logits, ld, u, temperature, top_k, top_p, min_p, tokens, logprob, V, sh, half};
   // Rows for every SM and more: some on each SM, they load and compute in turn (from
   // L2 after a row's first pass).  Fewer: a row's later passes from shared memory.
+  // Measured, us, staged / four an SM, 32768 logits, top-k 50 with top-p 0.95: 148 rows 16.4 / 22.0,
+  // 149 rows 25.6 / 21.5, 592 rows 54 / 32.  Top-p alone: 148 rows 64 / 104, 296 rows 112 / 151, 592
+  // rows 184 / 148; without a filter 149 rows 32 / 40, 400 rows 48 / 42: those two would turn over
+  // at some 400 rows, but what a row asks for is not known here.
   if (M > device_sm_count()) return launch_t<256, false>(p, M, 8 * kPart * 8, stream);
   const size_t smem = 16 * kPart * 8 + ((size_t)V + 7) / 4 * 16;
   if (smem <= kStageBytes) return launch_t<512, true>(p, M, smem, stream);

@@ -641,7 +641,13 @@ nc_status tree_mask_launch(const int32_t* parents, uint32_t* mask, int B, int N,
 // head 9.1 / 14.8, 14.0 / 17.0, 27.0 / 23.4; 64 rows 12.6 / 15.0, 18.7 / 17.3,
 // 41.6 / 23.9; 128 rows 14.8 / 15.7, 31.7 / 17.9, 73.4 / 25.3; 16 rows of the
 // cache, 12 kv heads, 32 rows: 19.3 / 24.3, 55.6 / 35.4, 180 / 80.  The lengths
-// are not known here; half of what the cache may hold stands for them.
+// are not known here; half of what the cache may hold stands for them.  What that
+// costs: more than 32 rows over lengths that stay short, whatever T_max, take the
+// tcgen05 kernel at 200 keys of 64 rows 14.5 / 15.4 (D = 128) and 11.3 / 14.5 (64),
+// of 128 rows 15.0 / 16.1 and 11.5 / 14.9 (T_max 512 to 4096); the kernels meet at
+// some 500 keys, for 64 rows of D = 64 between 1000 and 4000.
+// The tcgen05 kernel is out where a CTA's plan would not hold the rows of the cache
+// (more than 1024), a group has more than 128 heads or the window is 128 keys or less.
 static bool use_tc(int B, int N, int H, int Hkv, int D, int T_max, int window) {
   const int rows = N * (H / Hkv);
   const int keys = window > 0 && window < T_max ? window : T_max;

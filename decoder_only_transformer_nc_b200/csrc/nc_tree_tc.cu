@@ -54,7 +54,7 @@ namespace tree_tc {
 constexpr int BM = 128, BKV = 128;
 constexpr int NUM_THREADS = 64 + 256;
 constexpr int ATOM = 128 * 128;  // bytes of one [128 rows][64 x 16-bit] swizzle tile
-constexpr int kMaxB = 1024;      // rows whose tile counts a CTA keeps
+constexpr int kMaxB = 1024;      // rows whose tile counts a CTA keeps: 8 KB beside the tiles' 192 (D = 128)
 constexpr float kRescaleLog2 = 8.0f;
 // Weights are held times 2^7: with the 2^8 that they may grow they stay under fp16's
 // 65504, and one is lost below 2^-32 of the largest, not 2^-25: 2^22 keys of those weigh

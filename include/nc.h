@@ -290,7 +290,8 @@ nc_status nc_decode_step_dev(const nc_config* cfg, const nc_weights* w, const in
  * the caller samples a token at every node (nc_sample over the B * N rows), and
  * nc_accept_tree finds the path that the samples confirm and moves its keys and
  * values into the cache.  N = 1 is a decode step whose rows have lengths of
- * their own.  The session is nc_prefill's (cfg->fp8 must be 0); any
+ * their own (its attention is nc_tree_attention's, whose weights meet V in 16 bits;
+ * nc_decode_step's stay fp32).  The session is nc_prefill's (cfg->fp8 must be 0); any
  * n_head / n_kv_head is taken. */
 
 /* Bytes of the workspace of nc_decode_tree / nc_accept_tree (0 on bad input).
@@ -631,7 +632,8 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * over the committed keys t < lens[b] with lens[b] + depth_i - t < window and
  * the drafted keys j in mask_i with depth_i - depth_j < window (window <= 0:
  * all).  A node whose own bit is clear is unused: output 0, and its drafted K/V
- * are not read.  q: node n of row b at q + (b N + n) q_row_stride, H heads of D
+ * are not read.  Scores and sums are fp32; a weight enters the product with V in
+ * format dtype (rounded by half a step of it).  q: node n of row b at q + (b N + n) q_row_stride, H heads of D
  * (q_row_stride >= H D, a multiple of 8); kv [B, N, 2, Hkv, D]; cache
  * [B, T_max, 2, Hkv, D]; out [B, N, H, D]; 16-bit in format dtype.  lens [B] is
  * clamped to [0, T_max]; positions at and past it are not read.  D in {64,
@@ -680,8 +682,9 @@ nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const ui
  * clamped to [0, 1] (NaN: 0); 1 takes the last kept token.  NaN logits count as
  * -inf, which is never sampled; a row of those alone gives token -1 and logprob
  * -inf.  The largest logit weighs 1 also where it is +inf.  logprob may be NULL.
- * The token is that of weights rounded to an absolute unit of V / 2^62 (2^-47 at
- * V <= 32768; smaller ones count as 0) and exact sums, the same run to run.
+ * The token is that of weights rounded to units of 2^-51, or from V > 2048 on of
+ * P / 2^62, P the power of two at or above V (2^-47 at 32768, 2^-42 at 2^20; under
+ * half a unit counts as 0), and exact sums, the same run to run.
  * logprob may come from fp32 weights: the mass in it is within 4.5e-7 of each
  * weight, relative (a few 1e-8 in practice).  A row whose copy to the SM does not
  * arrive in time gives token -1 and logprob NaN.  tokens and logprob may overlap

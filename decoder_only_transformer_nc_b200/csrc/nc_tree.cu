@@ -85,12 +85,14 @@ __global__ void __launch_bounds__(kMaxNodes) tree_mask_kernel(const int32_t* __r
 // four tiles a CTA, each of them waited for at a barrier).  The products
 // run on m16n8k16 with fp32 accumulation; P enters P V in the 16-bit format of
 // the inputs (half a step of each weight, relative; the row's sum keeps them in
-// fp32), as in the attention kernels of the whole forward, and held times 2^15:
-// fp16's numbers end at 2^-24, and the weights of a long cache may all be below
-// that beside one large one.  (nc_decode_step's attention keeps its weights in fp32.)
+// fp32), as in the attention kernels of the whole forward; in fp16, whose numbers end
+// at 2^-24, times 2^15: the weights of a long cache may all be below that beside one
+// large one.  (nc_decode_step's attention keeps its weights in fp32.)
 constexpr int kTK = 64;      // keys per tile
 constexpr int kStages = 3;   // tiles in flight
-constexpr float kLift = 15.0f;  // weights (at most 1) times 2^15 stay under fp16's 65504
+// fp16: weights (at most 1) times 2^15 stay under 65504.  bf16 has fp32's range, for the
+// weights and for V, which may leave no room for a factor.
+constexpr float lift(bool f16) { return f16 ? 15.0f : 0.0f; }
 
 struct TreeAttnParams {
   const uint16_t* q;      // [B][N] rows of H heads, q_stride elements apart
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(128) tree_attn_kernel(const TreeAttnParams p) 
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float ms = mx == -INFINITY ? 0.0f : mx;  // nothing visible yet: every p is 0
-      const float a = ex2(m[h] - ms), mp = ms - kLift;  // the sum and O carry the factor too
+      const float a = ex2(m[h] - ms), mp = ms - lift(F16);  // the sum and O carry the factor too
       float ps = 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {

@@ -28,7 +28,7 @@
 // memory: S_0, S_1 (128 columns each; P replaces the first half in 16 bits),
 // O_0, O_1 (D columns each).  O is rescaled only when the running maximum grows
 // by more than 2^8, as in the other attention kernels.  P enters P V in 16 bits (the
-// row's sum keeps it in fp32), times 2^kLift (see there).
+// row's sum keeps it in fp32), in fp16 times a power of two (see log2_lift).
 // Measured, in a graph: 32 rows of 64 nodes, 16 heads on 4, 3000 to 8100 positions
 // of 128: 112 us for 385 MB and 93 GFLOP (59 us at the copy rate, 57 us at the tensor
 // rate, which no overlap takes below the larger): 3.4 TB/s and 830 TFLOP/s.  The
@@ -56,10 +56,11 @@ constexpr int NUM_THREADS = 64 + 256;
 constexpr int ATOM = 128 * 128;  // bytes of one [128 rows][64 x 16-bit] swizzle tile
 constexpr int kMaxB = 1024;      // rows whose tile counts a CTA keeps: 8 KB beside the tiles' 192 (D = 128)
 constexpr float kRescaleLog2 = 8.0f;
-// Weights are held times 2^7: with the 2^8 that they may grow they stay under fp16's
+// In fp16 weights are held times 2^7: with the 2^8 that they may grow they stay under
 // 65504, and one is lost below 2^-32 of the largest, not 2^-25: 2^22 keys of those weigh
 // no more than half a rounding step of fp16 (at 2^-25 they would weigh an eighth).
-constexpr float kLift = 7.0f;
+// bf16 has fp32's range, for the weights and for V, which may leave no room for a factor.
+constexpr float log2_lift(bool f16) { return f16 ? 7.0f : 0.0f; }
 
 template <int D>
 struct Geo {
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int r = (int)(quarter * 32 + lane);  // this thread's row of the tile
     const uint32_t lane_off = (quarter * 32u) << 16;
     const uint32_t scol = tmem + lane_off + w * BKV, ocol = tmem + lane_off + O_COL;
-    const float lift = kLift / p.scale_log2, thresh = kRescaleLog2 / p.scale_log2 + lift;
+    const float lift = log2_lift(F16) / p.scale_log2, thresh = kRescaleLog2 / p.scale_log2 + lift;
     const int W = (p.N + 31) / 32;
     int gt = 0, n = 0, gs = 0, go[2] = {0, 0};
     bool ok = true;

@@ -52,6 +52,27 @@ def test_far_weights_count(gpu, N, H, T, first, D, dt):
     assert err.max() <= rel, f"relative error {err.max():.3g}"
 
 
+@pytest.mark.parametrize("N,H,T", [(4, 2, 300), (40, 2, 300), (40, 4, 700)])
+def test_values_near_the_end_of_bf16(gpu, N, H, T):
+    """V of 1e38 at a key whose weight is nearly all of its row's: what fp32 has room for, without a factor.  The other
+    keys, 30 in the exponent below, have V of 1.  Errors: the weight (1) is exact, the output is rounded once (2^-9),
+    the division and the sum add 2^-22."""
+    B, D = 2, 64
+    q = torch.zeros((B, N, H, D))
+    q[..., 0] = 16
+    kv, cache = torch.zeros((B, N, 2, 1, D)), torch.zeros((B, T, 2, 1, D))
+    kv[:, :, 1] = cache[:, :, 1] = 1.0
+    cache[:, T // 2, 0, 0, 0] = 15.0
+    cache[:, T // 2, 1] = 1e38
+    q, kv, cache = (x.bfloat16().to(DEV) for x in (q, kv, cache))
+    mask = o64.tree_mask(np.tile(np.arange(N, dtype=np.int32) - 1, (B, 1)))
+    out = torch.empty_like(q)
+    gpu.tree_attention(q, kv, cache, torch.full((B,), T, dtype=torch.int32, device=DEV),
+                       torch.from_numpy(mask.view(np.int32)).to(DEV), out, 0)
+    want = cache[0, T // 2, 1, 0, 0].double().item()
+    assert ((out.double() - want).abs() <= want * 2.0 ** -8).all()
+
+
 # ------------------------------------------------------------------ sampling: weights under the unit
 
 def _sample(gpu, l, u, **kw):

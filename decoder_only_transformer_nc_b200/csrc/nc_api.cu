@@ -1107,6 +1107,13 @@ bool overlap(const Span& a, const Span& b) {
   return a.at && b.at && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
 }
 
+// The same against rows of `bytes`, `stride` bytes apart: what lies between them is free.
+bool overlap_rows(const Span& a, const void* first, int64_t rows, int64_t stride, int64_t bytes) {
+  if (rows < 1 || !overlap(a, {first, (rows - 1) * stride + bytes})) return false;
+  const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(a.at) - reinterpret_cast<uintptr_t>(first));
+  return off < 0 || off % stride < bytes || off % stride + a.bytes > stride;
+}
+
 // Whether an output overlaps an input or another output.
 bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
   for (const Span* o = outs.begin(); o != outs.end(); ++o) {
@@ -1164,11 +1171,11 @@ nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint1
   if (need > 0 && (!workspace || ws_bytes < need)) return NC_ERR_WORKSPACE;
   // out may be q itself: a row of q is read by the CTAs of its kv head alone, before its output is written
   const int64_t BN = (int64_t)B * N, row = (int64_t)2 * Hkv * D * 2;
-  const Span o{out, BN * H * D * 2}, query{q, B > 0 ? ((BN - 1) * q_row_stride + (int64_t)H * D) * 2 : 0};
-  if (any_overlap({o, {need > 0 ? workspace : nullptr, (int64_t)need}},
+  const Span o{out, BN * H * D * 2}, w{need > 0 ? workspace : nullptr, (int64_t)need};
+  auto on_q = [&](const Span& s) { return overlap_rows(s, q, BN, q_row_stride * 2, (int64_t)H * D * 2); };
+  if (any_overlap({o, w},
                   {{kv, BN * row}, {cache, (int64_t)B * T_max * row}, {lens, (int64_t)B * 4}, {mask, BN * ((N + 31) / 32) * 4}}) ||
-      (overlap(o, query) && (out != q || q_row_stride != (int64_t)H * D)) ||
-      (need > 0 && overlap(query, {workspace, (int64_t)need})))
+      (on_q(o) && (out != q || q_row_stride != (int64_t)H * D)) || on_q(w))
     return NC_ERR_INVALID_ARG;
   if (nc_status s = device_ok()) return s;
   return tree_attention_launch(q, q_row_stride, kv, cache, lens, mask, out, B, N, H, Hkv, D, T_max, window,
@@ -1204,10 +1211,12 @@ nc_status nc_sample(const float* logits, int64_t row_stride, const float* u, con
   // a row reads its numbers before it writes its own: the same array will do, one shifted by rows will not
   const int64_t rows = (int64_t)M * 4;
   const Span tok{tokens, rows}, lp{logprob, rows};
-  if (any_overlap({tok, lp}, {{logits, M > 0 ? (((int64_t)M - 1) * row_stride + V) * 4 : 0}})) return NC_ERR_INVALID_ARG;
-  for (const void* in : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p})
-    for (const Span& out : {tok, lp})
+  if (overlap(tok, lp)) return NC_ERR_INVALID_ARG;
+  for (const Span& out : {tok, lp}) {
+    if (overlap_rows(out, logits, M, row_stride * 4, (int64_t)V * 4)) return NC_ERR_INVALID_ARG;
+    for (const void* in : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p})
       if (overlap(out, {in, rows}) && out.at != in) return NC_ERR_INVALID_ARG;
+  }
   if (nc_status s = device_ok()) return s;
   return sample_launch(logits, row_stride, u, temperature, top_k, top_p, min_p, tokens, logprob, M, V, S(stream));
 }

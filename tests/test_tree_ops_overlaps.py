@@ -139,3 +139,21 @@ def test_sample_overlaps(nclib):
             base = _places(names)[i]
             assert code(**{o: base}) == (1 if i in ("tokens", "logprob") else 8), (o, i)
             assert code(**{o: base + 4}) == 1 and code(**{o: base - 4}) == 1 and code(**{o: base + M * 4}) == 8, (o, i)
+    # between two rows of the logits there is room
+    at = _places(names)["logits"]
+    assert code(tokens=at + V * 4) == 8 and code(tokens=at + (ld + V) * 4, logprob=at + (ld - M) * 4) == 8
+    assert code(tokens=at + V * 4 - 4) == 1 and code(tokens=at + (ld - M + 1) * 4) == 1
+    assert code(tokens=at - M * 4) == 8 and code(tokens=at - M * 4 + 4) == 1
+
+
+def test_tree_attention_output_between_the_queries(nclib):
+    L = nclib.lib()
+    B, N, H, Hkv, D, T, stride = 1, 2, 2, 2, 64, 32, 512  # q: 256 bytes of every 1024; out: 512 bytes
+    names = ["q", "kv", "cache", "lens", "mask", "out"]
+
+    def code(out):
+        a = _places(names)
+        return L.nc_tree_attention(a["q"], stride, a["kv"], a["cache"], a["lens"], a["mask"], out, B, N, H, Hkv, D, T, 0, 1, None, 0,
+                                   None, None)
+
+    assert [code(P + d) for d in (0, 240, 256, 512, 528, 1024, 1264, 1280, -512, -496)] == [1, 1, 8, 8, 1, 1, 1, 8, 8, 1]

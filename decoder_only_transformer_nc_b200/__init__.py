@@ -361,6 +361,8 @@ class Session:
         ws = torch.empty(max(1, lib().nc_prefill_workspace_bytes(ctypes.byref(cfg), B, T)), dtype=torch.uint8,
                          device=tokens.device)
         logits = torch.empty((B, T, cfg.vocab), dtype=torch.float32, device=tokens.device) if want_logits else None
+        if stream is not None:
+            self._used_on(stream, ws)
         _check(lib().nc_prefill(ctypes.byref(cfg), ctypes.byref(self.model.weights), _ptr(tokens), B, T,
                                 _ptr(logits), _ptr(self.buffer), self.buffer.numel(), self.T_max, _ptr(ws),
                                 ws.numel(), _stream(stream)), "nc_prefill")

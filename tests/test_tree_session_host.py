@@ -32,3 +32,16 @@ def test_a_tree_held_by_the_session_outlives_calls_on_another_stream(session):
     smp = torch.zeros((2, 3), dtype=torch.int32)
     sess.accept_tree(smp)
     assert want | {ws, smp.data_ptr()} <= set(sum(used, []))
+
+
+def test_prefill_marks_its_workspace(session, nclib):
+    """Its workspace is freed when the call returns, maybe before the stream has come to it."""
+    sess, used = session
+    made = []
+    empty = torch.empty
+    torch_empty = lambda *a, **k: made.append(empty(*a, **k)) or made[-1]  # noqa: E731
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(torch, "empty", torch_empty)
+        with pytest.raises(nclib.NcError):  # the launch: the session's buffer is a stand-in
+            sess.prefill(torch.zeros((2, 3), dtype=torch.int32), stream=SimpleNamespace(cuda_stream=0))
+    assert len(made) == 1 and made[0].data_ptr() in sum(used, [])

@@ -633,8 +633,9 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * the drafted keys j in mask_i with depth_i - depth_j < window (window <= 0:
  * all).  A node whose own bit is clear is unused: output 0, and its drafted K/V
  * are not read.  Scores and sums are fp32; a weight enters the product with V in
- * format dtype (rounded by half a step of it).  q: node n of row b at q + (b N + n) q_row_stride, H heads of D
- * (q_row_stride >= H D, a multiple of 8); kv [B, N, 2, Hkv, D]; cache
+ * format dtype (rounded by half a step of it; in fp16 one under 2^-32 of its row's
+ * largest may count as 0).  q: node n of row b at q + (b N + n) q_row_stride, H
+ * heads of D (q_row_stride >= H D, a multiple of 8); kv [B, N, 2, Hkv, D]; cache
  * [B, T_max, 2, Hkv, D]; out [B, N, H, D]; 16-bit in format dtype.  lens [B] is
  * clamped to [0, T_max]; positions at and past it are not read.  D in {64,
  * 128}, 1 <= N <= 128, 1 <= T_max <= 2^22, B <= 65535, H <= 4096.  Bits of mask
@@ -642,8 +643,8 @@ nc_status nc_tree_mask(const int32_t* parents, uint32_t* mask, int B, int N, voi
  * and of used nodes must be finite.  workspace: at least
  * nc_tree_attention_workspace_bytes bytes, 16-byte aligned (NULL where that is
  * 0); calls that overlap in time need one each.  out may be q (of q_row_stride
- * H D); else neither it nor the workspace may overlap an input.  dev_status (or NULL) gets
- * NC_DEV_TIMEOUT if a pipeline wait ran out (out is not valid then).  The result
+ * H D); else neither it nor the workspace may overlap an input.  dev_status (or
+ * NULL) gets NC_DEV_TIMEOUT if a pipeline wait ran out (out is not valid then).  The result
  * is the same run to run. */
 size_t nc_tree_attention_workspace_bytes(int B, int N, int H, int Hkv, int D, int T_max, int window);
 nc_status nc_tree_attention(const uint16_t* q, int64_t q_row_stride, const uint16_t* kv, const uint16_t* cache,
@@ -686,7 +687,7 @@ nc_status nc_tree_accept(const int32_t* tokens, const int32_t* parents, const ui
  * P / 2^62, P the power of two at or above V (2^-47 at 32768, 2^-42 at 2^20; under
  * half a unit counts as 0), and exact sums, the same run to run.
  * logprob may come from fp32 weights: the mass in it is within 4.5e-7 of each
- * weight, relative (a few 1e-8 in practice).  A row whose copy to the SM does not
+ * weight, relative (a few 1e-8 in practice), and within V half units.  A row whose copy to the SM does not
  * arrive in time gives token -1 and logprob NaN.  tokens and logprob may overlap
  * neither the logits nor each other, and of the arrays per row only one as a whole.
  * 1 <= V <= 2^24. */
